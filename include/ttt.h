@@ -248,6 +248,86 @@ int ttt_linear_chunked_bidir_noalloc(const void* q, const void* k, const void* v
                                      int dtype, void* stream);
 size_t ttt_linear_chunked_bidir_noalloc_max_bytes(void);
 
+/* --------------------------------------------------------------------------------------
+ * TTT-Linear, full batch, with an orthogonalised inner update: the step goes along the
+ * orthogonal factor of the gradient instead of the gradient itself.  Per unit u = b*H + h:
+ *     g  = (1/N) (K^T K W0[h] - K^T V),   W* = W0[h] - eta * NS(g),   O = Q W*,
+ * with NS the Newton-Schulz steps of ttt_orthogonalize (same steps, a, b, c, eps, scale 1).
+ * Tensors, sizes and w_star as for ttt_linear_fullbatch; the workspace is always needed.  The
+ * step's length does not depend on the gradient's: eta 0.02 to 0.5 is usual.  Forward only.
+ * Sizes: 1 <= d <= 128, B*H <= 65535.  bf16 with d = 64 runs the tensor-core kernels.
+ * ------------------------------------------------------------------------------------ */
+size_t ttt_linear_fullbatch_orth_workspace_bytes(int B, int H, int N, int d, int dtype);
+int ttt_linear_fullbatch_orth(const void* q, const void* k, const void* v, const float* w0, void* out,
+                              float* w_star, int B, int H, int N, int d, float eta, int steps, float a,
+                              float b, float c, float eps, int dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * The orthogonal factor of an update by Newton-Schulz products, for the gradients of weights
+ * (dw0 of ttt_linear_fullbatch_bwd, projections).  Per matrix u, x[u] in R^{m x n}:
+ *     X = x / max(|x|_F, eps);   `steps` times:  A = X X^T,  X <- a X + (b A + c A^2) X;
+ *     out = scale * X
+ * which sends each singular value s of X to a s + b s^3 + c s^5 at every step and keeps the
+ * singular vectors; the usual quintic (a, b, c) = (3.4445, -4.7750, 2.0315) brings them near 1
+ * in five steps.  A tall matrix (m > n) is taken transposed.
+ *   x, out : [U, m, n] dtype (out may be x)
+ * A zero matrix stays zero; one with a NaN or an infinity becomes NaN throughout.  fp32 results
+ * are good to about 1e-6 of their norm, bf16 ones to their rounding.  Errors: steps outside 1..64,
+ * eps <= 0 or a non-finite number is TTT_ERR_INVALID_ARG; coefficients under which a value in
+ * [0, 1] leaves [-2, 2] on the way (the iteration would run away), U > 65535 or m, n > 32768 is
+ * TTT_ERR_UNSUPPORTED.  The workspace is always needed.
+ * ------------------------------------------------------------------------------------ */
+size_t ttt_orthogonalize_workspace_bytes(int U, int m, int n, int dtype);
+int ttt_orthogonalize(const void* x, void* out, int U, int m, int n, int steps, float a, float b, float c,
+                      float eps, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * Layer norm of token rows (the Norm of the block wrapper, ViT^3 blog: Norm -> TTT block ->
+ * Residual) and its backward pass.  Per row of C features, mu its mean, v its mean square
+ * deviation, xh = (x - mu) / sqrt(v + eps):
+ *     y = xh * gamma + beta
+ *     dx = (t - mean(t) - xh * mean(t * xh)) / sqrt(v + eps),  t = dy * gamma
+ *     dgamma = sum over rows of dy * xh,   dbeta = sum over rows of dy
+ *   x, y, dy, dx : [rows, C] dtype (y may be x; dx may be dy or x)
+ *   gamma, beta, dgamma, dbeta : [C] fp32; beta and dbeta may be NULL
+ * Statistics are fp32 and are formed again by the backward pass; sums over rows have a fixed
+ * order (deterministic).  Squares of a row's deviations have to fit fp32.  C <= 16384, else
+ * TTT_ERR_UNSUPPORTED.  The backward pass needs a workspace.
+ * ------------------------------------------------------------------------------------ */
+int ttt_layernorm(const void* x, const float* gamma, const float* beta, void* y, int rows, int C, float eps,
+                  int dtype, void* stream);
+size_t ttt_layernorm_bwd_workspace_bytes(int rows, int C, int dtype);
+int ttt_layernorm_bwd(const void* dy, const void* x, const float* gamma, void* dx, float* dgamma, float* dbeta,
+                      int rows, int C, float eps, int dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * Rotary positions of Q and K with several axes (row and column of the token grid, time for
+ * video), ahead of the TTT layer.  The first axis_dims[0] features of a head turn with the
+ * token's position on axis 0, the next axis_dims[1] with axis 1, ...; the rest pass unchanged.
+ * In a section of width s, pair j < s/2 turns by p * base^(-2 j / s):
+ *     (x, y) -> (x cos - y sin, y cos + x sin),
+ * the pair being features (j, j + s/2) of the section, or (2j, 2j + 1) with `interleaved`.
+ * `inverse` turns back: that is also the backward pass (dq, dk in, gradients of q, k out).
+ *   q, k, q_out, k_out : [B, H, N, d] dtype; k and k_out may both be NULL
+ *   pos       : fp32 [N, axes], or [B, N, axes] with pos_batched; fractions are allowed.  NULL:
+ *   grid      : HOST array of `axes` sizes whose product is N; token n has the raster-order
+ *               coordinates of cell n (last axis fastest).  Exactly one of pos and grid is given.
+ *   axis_dims : HOST array of `axes` even widths, their sum at most d
+ *   strides   : HOST array of 12 element strides, (b, h, n) of q, k, q_out, k_out, or NULL for
+ *               dense [B, H, N, d].  The features of a head are adjacent.  Inputs may have
+ *               stride 0; outputs may not address an element twice.  These tensors need only the
+ *               alignment of their element type (16-byte rows are the fast ones).
+ * An output may be its own input (same pointer, same strides); otherwise outputs overlap
+ * nothing.  Angles are reduced in fp64, so far positions lose nothing.  axes <= 4, d <= 512,
+ * B, H <= 65535, else TTT_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------------------ */
+int ttt_rope(const void* q, const void* k, void* q_out, void* k_out, const float* pos, int pos_batched,
+             const int* grid, const int* axis_dims, int axes, int B, int H, int N, int d, double base,
+             int interleaved, int inverse, const long long* strides, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

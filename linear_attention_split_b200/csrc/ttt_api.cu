@@ -25,6 +25,9 @@
 #include "apply_tc.cuh"
 #include "chunked_tc.cuh"
 #include "mlp_tc.cuh"
+#include "norm.cuh"
+#include "rope.cuh"
+#include "orth.cuh"
 
 namespace {
 
@@ -766,9 +769,162 @@ int noalloc_scratch(void** addr) {
     return TTT_OK;
 }
 
+// ------------------------------------------------------------------ layer norm ---------
+// Threads of a row and vectors per thread (NV): 16-byte loads where every row starts on a
+// 16-byte boundary, single elements otherwise.
+struct NormPlan {
+    lnorm::Shape s;
+    int vec, nv;
+};
+NormPlan norm_plan(int C, int dtype) {
+    NormPlan p;
+    const int full = dtype == TTT_BF16 ? 8 : 4;
+    p.vec = C % full == 0 ? full : 1;
+    const int vecs = C / p.vec, most = lnorm::MAX_EPT / p.vec;
+    p.nv = most;
+    while (p.nv > 1 && p.nv * 16 > vecs) p.nv /= 2;  // short rows: a lane per vector first
+    const int need = (vecs + p.nv - 1) / p.nv;
+    if (need <= 32) {
+        p.s.lanes = 1;
+        while (p.s.lanes < need) p.s.lanes *= 2;
+        p.s.warps = 1;
+    } else {
+        p.s.lanes = 32;
+        p.s.warps = (need + 31) / 32;
+    }
+    const int tpr = p.s.lanes * p.s.warps;
+    p.s.threads = tpr >= lnorm::THREADS ? tpr : lnorm::THREADS / tpr * tpr;
+    return p;
+}
+template <typename F>
+int norm_dispatch(const NormPlan& p, int dtype, F f) {
+    using bf = __nv_bfloat16;
+    using std::integral_constant;
+    if (dtype == TTT_BF16) {
+        if (p.vec == 8) return p.nv == 1 ? f(bf(), integral_constant<int, 8>(), integral_constant<int, 1>())
+                                         : f(bf(), integral_constant<int, 8>(), integral_constant<int, 2>());
+        switch (p.nv) {
+            case 1: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 1>());
+            case 2: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 2>());
+            case 4: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 4>());
+            case 8: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 8>());
+            default: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 16>());
+        }
+    }
+    if (p.vec == 4) {
+        switch (p.nv) {
+            case 1: return f(float(), integral_constant<int, 4>(), integral_constant<int, 1>());
+            case 2: return f(float(), integral_constant<int, 4>(), integral_constant<int, 2>());
+            default: return f(float(), integral_constant<int, 4>(), integral_constant<int, 4>());
+        }
+    }
+    switch (p.nv) {
+        case 1: return f(float(), integral_constant<int, 1>(), integral_constant<int, 1>());
+        case 2: return f(float(), integral_constant<int, 1>(), integral_constant<int, 2>());
+        case 4: return f(float(), integral_constant<int, 1>(), integral_constant<int, 4>());
+        case 8: return f(float(), integral_constant<int, 1>(), integral_constant<int, 8>());
+        default: return f(float(), integral_constant<int, 1>(), integral_constant<int, 16>());
+    }
+}
+// blocks of the backward pass: two per SM, fewer for few rows
+int norm_bwd_blocks(const NormPlan& p, int rows) {
+    DeviceInfo* dev = nullptr;
+    const int sms = current_device(&dev) == TTT_OK ? dev->sms : 148;
+    const int rpb = p.s.rows_per_block();
+    return std::min(2 * sms, (rows + rpb - 1) / rpb);
+}
+int norm_check(const void* a, const void* b, const void* c, const float* gamma, int rows, int C, float eps, int dtype) {
+    if (!a || !b || !c || !gamma) return TTT_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(c) || !aligned16(gamma)) return TTT_ERR_INVALID_ARG;
+    if (dtype != TTT_F32 && dtype != TTT_BF16) return TTT_ERR_INVALID_ARG;
+    if (rows <= 0 || C <= 0 || !std::isfinite(eps) || eps < 0.f) return TTT_ERR_INVALID_ARG;
+    return C > lnorm::MAX_COLS ? TTT_ERR_UNSUPPORTED : TTT_OK;
+}
+
+// ------------------------------------------------------------------ rotary positions ----
+// Whether a tensor [B][H][N] of d adjacent features with these strides has no element twice.
+bool rope_strides_disjoint(const long long* st, int B, int H, int N, int d) {
+    struct Dim {
+        long long stride, size;
+    } dims[3] = {{st[0], B}, {st[1], H}, {st[2], N}};
+    std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    long long span = d;
+    for (const Dim& x : dims) {
+        if (x.size == 1) continue;
+        if (x.stride < span) return false;
+        span += x.stride * (x.size - 1);
+    }
+    return true;
+}
+
+// ------------------------------------------------------------------ orthogonal update ---
+// Whether the iteration stays bounded: every value in [0, 1] (the singular values of a matrix of
+// Frobenius norm 1) keeps to at most 2 through all steps, and |b s^2| + |c s^4| to at most 32.
+bool orth_coef_ok(double a, double b, double c, int steps) {
+    double top = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        if (std::fabs(b) * top * top + std::fabs(c) * top * top * top * top > 32.0) return false;
+        double next = 0.0;
+        for (int i = 0; i <= 2048; ++i) {
+            const double s = top * i / 2048.0;
+            next = std::max(next, std::fabs(s * (a + s * s * (b + c * s * s))));
+        }
+        if (!(next <= 2.0)) return false;
+        top = next;
+    }
+    return true;
+}
+struct OrthPlan {
+    int M, N, tall, parts;
+    size_t part, y, z, a, b, total;  // byte offsets of the workspace's parts, and its size
+};
+OrthPlan orth_plan(long long U, int m, int n) {
+    OrthPlan p;
+    p.tall = m > n;
+    p.M = std::min(m, n);
+    p.N = std::max(m, n);
+    const long long mn = (long long)m * n;
+    p.parts = (int)std::min<long long>(orth::MAX_PARTS, (mn + 4095) / 4096);
+    p.part = 0;
+    p.y = align256((size_t)U * p.parts * 8);
+    p.z = p.y + align256((size_t)U * mn * 4);
+    p.a = p.z + align256((size_t)U * mn * 4);
+    p.b = p.a + align256((size_t)U * p.M * p.M * 4);
+    p.total = p.b + align256((size_t)U * p.M * p.M * 4);
+    return p;
+}
+int orth_check(int steps, float a, float b, float c, float eps) {
+    if (steps <= 0 || steps > 64) return TTT_ERR_INVALID_ARG;
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !std::isfinite(eps) || eps <= 0.f)
+        return TTT_ERR_INVALID_ARG;
+    return orth_coef_ok(a, b, c, steps) ? TTT_OK : TTT_ERR_UNSUPPORTED;
+}
+// out = scale * (Newton-Schulz steps of x); T: the type of x and out
+template <typename T>
+int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, float b, float c, float eps,
+             float scale, void* workspace, cudaStream_t st) {
+    const OrthPlan p = orth_plan(U, m, n);
+    const long long mn = (long long)m * n;
+    char* w = static_cast<char*>(workspace);
+    double* part = reinterpret_cast<double*>(w + p.part);
+    float *y = reinterpret_cast<float*>(w + p.y), *z = reinterpret_cast<float*>(w + p.z);
+    float *g = reinterpret_cast<float*>(w + p.a), *h = reinterpret_cast<float*>(w + p.b);
+    const dim3 each((unsigned)((mn + orth::TPB - 1) / orth::TPB), (unsigned)U);
+    orth::square_kernel<T><<<dim3((unsigned)p.parts, (unsigned)U), orth::TPB, 0, st>>>(x, part, mn);
+    orth::start_kernel<T><<<each, orth::TPB, 0, st>>>(x, part, y, p.parts, p.M, p.N, p.tall, eps);
+    const dim3 gram((p.M + 63) / 64, (p.M + 63) / 64, (unsigned)U), rect((p.N + 63) / 64, (p.M + 63) / 64, (unsigned)U);
+    for (int k = 0; k < steps; ++k) {
+        orth::product_kernel<<<gram, orth::TPB, 0, st>>>(y, y, nullptr, g, p.M, p.M, p.N, 1, 1.f, 0.f);
+        orth::product_kernel<<<gram, orth::TPB, 0, st>>>(g, g, g, h, p.M, p.M, p.M, 1, c, b);
+        orth::product_kernel<<<rect, orth::TPB, 0, st>>>(h, y, y, z, p.M, p.N, p.M, 0, 1.f, a);
+        std::swap(y, z);
+    }
+    orth::end_kernel<T><<<each, orth::TPB, 0, st>>>(y, out, p.M, p.N, p.tall, scale);
+    return launched(3 + 3 * steps);
+}
+
 }  // namespace
 
-// ====================================================================== C ABI ==========
 extern "C" {
 
 const char* ttt_status_string(int status) {
@@ -1243,5 +1399,195 @@ int ttt_linear_chunked_bidir_noalloc(const void* q, const void* k, const void* v
 }
 
 size_t ttt_linear_chunked_bidir_noalloc_max_bytes(void) { return kNoAllocScratchBytes; }
+
+// ------------------------------------------------------------------ layer norm ---------
+int ttt_layernorm(const void* x, const float* gamma, const float* beta, void* y, int rows, int C, float eps, int dtype,
+                  void* stream) {
+    NvtxRange nvtx_range("ttt_layernorm");
+    if (int rc = norm_check(x, y, x, gamma, rows, C, eps, dtype)) return rc;
+    if (beta && !aligned16(beta)) return TTT_ERR_INVALID_ARG;
+    const NormPlan p = norm_plan(C, dtype);
+    const int rpb = p.s.rows_per_block();
+    return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv) {
+        using T = decltype(t);
+        lnorm::forward_kernel<T, vec(), nv()><<<(rows + rpb - 1) / rpb, p.s.threads, 0, static_cast<cudaStream_t>(stream)>>>(
+            static_cast<const T*>(x), gamma, beta, static_cast<T*>(y), rows, C, eps, (float)(1.0 / C), p.s);
+        return launched(1);
+    });
+}
+
+size_t ttt_layernorm_bwd_workspace_bytes(int rows, int C, int dtype) {
+    if (rows <= 0 || C <= 0 || C > lnorm::MAX_COLS) return 0;
+    return (size_t)norm_bwd_blocks(norm_plan(C, dtype), rows) * 2 * C * 4;
+}
+
+int ttt_layernorm_bwd(const void* dy, const void* x, const float* gamma, void* dx, float* dgamma, float* dbeta, int rows,
+                      int C, float eps, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("ttt_layernorm_bwd");
+    if (int rc = norm_check(dy, x, dx, gamma, rows, C, eps, dtype)) return rc;
+    if (!dgamma || !aligned16(dgamma) || (dbeta && !aligned16(dbeta))) return TTT_ERR_INVALID_ARG;
+    const size_t need = ttt_layernorm_bwd_workspace_bytes(rows, C, dtype);
+    if (workspace_bytes < need || !workspace) return TTT_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TTT_ERR_INVALID_ARG;
+    const NormPlan p = norm_plan(C, dtype);
+    const int blocks = norm_bwd_blocks(p, rows), rpb = p.s.rows_per_block();
+    const int smem = rpb > 1 ? rpb * 2 * C * 4 : 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    float* part = static_cast<float*>(workspace);
+    return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv) {
+        using T = decltype(t);
+        lnorm::backward_kernel<T, vec(), nv()><<<blocks, p.s.threads, smem, st>>>(
+            static_cast<const T*>(dy), static_cast<const T*>(x), gamma, static_cast<T*>(dx), part, rows, C, eps,
+            (float)(1.0 / C), p.s);
+        lnorm::finish_kernel<<<(2 * C + 31) / 32, 256, 0, st>>>(part, dgamma, dbeta, blocks, C);
+        return launched(2);
+    });
+}
+
+// ------------------------------------------------------------------ rotary positions ----
+int ttt_rope(const void* q, const void* k, void* q_out, void* k_out, const float* pos, int pos_batched, const int* grid,
+             const int* axis_dims, int axes, int B, int H, int N, int d, double base, int interleaved, int inverse,
+             const long long* strides, int dtype, void* stream) {
+    NvtxRange nvtx_range("ttt_rope");
+    if (!q || !q_out || !axis_dims || (k == nullptr) != (k_out == nullptr)) return TTT_ERR_INVALID_ARG;
+    if (dtype != TTT_F32 && dtype != TTT_BF16) return TTT_ERR_INVALID_ARG;
+    if (B <= 0 || H <= 0 || N <= 0 || d <= 0 || axes <= 0) return TTT_ERR_INVALID_ARG;
+    if (axes > rope::MAX_AXES || d > rope::MAX_D || B > 65535 || H > 65535) return TTT_ERR_UNSUPPORTED;
+    if (!std::isfinite(base) || base <= 0.0) return TTT_ERR_INVALID_ARG;
+    if ((pos == nullptr) == (grid == nullptr)) return TTT_ERR_INVALID_ARG;
+    const uintptr_t es = dtype == TTT_BF16 ? 2 : 4;
+    for (const void* t : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
+        if (reinterpret_cast<uintptr_t>(t) % es) return TTT_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(pos) % 4) return TTT_ERR_INVALID_ARG;
+    rope::Params p = {};
+    int at = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (axis_dims[a] <= 0 || axis_dims[a] % 2 || axis_dims[a] > d - at) return TTT_ERR_INVALID_ARG;
+        p.ax.at[a] = at;
+        p.ax.dims[a] = axis_dims[a];
+        for (int j = 0; j < axis_dims[a] / 2; ++j)
+            p.turns[at / 2 + j] = std::pow(base, -2.0 * j / axis_dims[a]) / 6.283185307179586476925286766559;
+        at += axis_dims[a];
+    }
+    if (grid) {
+        long long cells = 1;
+        for (int a = 0; a < axes; ++a) {
+            if (grid[a] <= 0) return TTT_ERR_INVALID_ARG;
+            p.ax.grid[a] = grid[a];
+            cells *= grid[a];
+            if (cells > N) return TTT_ERR_INVALID_ARG;
+        }
+        if (cells != N) return TTT_ERR_INVALID_ARG;
+    }
+    const long long dense[3] = {(long long)H * N * d, (long long)N * d, d};
+    const long long* s[4];
+    for (int t = 0; t < 4; ++t) {
+        s[t] = strides ? strides + 3 * t : dense;
+        if ((t & 1) && !k) continue;
+        if (s[t][0] < 0 || s[t][1] < 0 || s[t][2] < 0) return TTT_ERR_INVALID_ARG;
+        if (t >= 2 && !rope_strides_disjoint(s[t], B, H, N, d)) return TTT_ERR_INVALID_ARG;
+    }
+    if (q == q_out && (s[0][0] != s[2][0] || s[0][1] != s[2][1] || s[0][2] != s[2][2])) return TTT_ERR_INVALID_ARG;
+    if (k && k == k_out && (s[1][0] != s[3][0] || s[1][1] != s[3][1] || s[1][2] != s[3][2])) return TTT_ERR_INVALID_ARG;
+    p.pos = pos;
+    p.pos_b = pos && pos_batched ? (long long)N * axes : 0;
+    p.B = B;
+    p.H = H;
+    p.N = N;
+    p.d = d;
+    p.ax.n = axes;
+    p.ax.pairs = at / 2;
+    p.interleaved = interleaved != 0;
+    p.sign = inverse ? -1.f : 1.f;
+    rope::View* v[4] = {&p.qi, &p.ki, &p.qo, &p.ko};
+    for (int t = 0; t < 4; ++t) *v[t] = {s[t][0], s[t][1], s[t][2]};
+    DeviceInfo* dev = nullptr;
+    if (int rc = current_device(&dev)) return rc;
+    p.TN = std::max(1, std::min(16, 4096 / p.ax.pairs));
+    const int tiles = (N + p.TN - 1) / p.TN;
+    int hg = 1;
+    while (hg < H && (long long)tiles * B * hg < 2LL * dev->sms) ++hg;
+    const dim3 g((unsigned)tiles, (unsigned)std::min(hg, 65535), (unsigned)B);
+    const int smem = p.TN * p.ax.pairs * 8;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == TTT_BF16) {
+        using T = __nv_bfloat16;
+        rope::rope_kernel<T><<<g, rope::THREADS, smem, st>>>(static_cast<const T*>(q), static_cast<const T*>(k),
+                                                             static_cast<T*>(q_out), static_cast<T*>(k_out), p);
+    } else {
+        using T = float;
+        rope::rope_kernel<T><<<g, rope::THREADS, smem, st>>>(static_cast<const T*>(q), static_cast<const T*>(k),
+                                                             static_cast<T*>(q_out), static_cast<T*>(k_out), p);
+    }
+    return launched(1);
+}
+
+// ------------------------------------------------------------------ orthogonal update ---
+size_t ttt_orthogonalize_workspace_bytes(int U, int m, int n, int dtype) {
+    if (U <= 0 || m <= 0 || n <= 0 || (dtype != TTT_F32 && dtype != TTT_BF16)) return 0;
+    return orth_plan(U, m, n).total;
+}
+
+int ttt_orthogonalize(const void* x, void* out, int U, int m, int n, int steps, float a, float b, float c, float eps,
+                      float scale, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("ttt_orthogonalize");
+    if (!x || !out || !aligned16(x) || !aligned16(out)) return TTT_ERR_INVALID_ARG;
+    if (dtype != TTT_F32 && dtype != TTT_BF16) return TTT_ERR_INVALID_ARG;
+    if (U <= 0 || m <= 0 || n <= 0 || !std::isfinite(scale)) return TTT_ERR_INVALID_ARG;
+    if (int rc = orth_check(steps, a, b, c, eps)) return rc;
+    if (U > 65535 || m > 32768 || n > 32768) return TTT_ERR_UNSUPPORTED;
+    const size_t need = ttt_orthogonalize_workspace_bytes(U, m, n, dtype);
+    if (workspace_bytes < need || !workspace) return TTT_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TTT_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == TTT_BF16)
+        return orth_run(static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(out), U, m, n, steps, a, b, c,
+                        eps, scale, workspace, st);
+    return orth_run(static_cast<const float*>(x), static_cast<float*>(out), U, m, n, steps, a, b, c, eps, scale,
+                    workspace, st);
+}
+
+// ------------------------------------------------------------------ TTT-Linear, orthogonalised step
+size_t ttt_linear_fullbatch_orth_workspace_bytes(int B, int H, int N, int d, int dtype) {
+    if (B <= 0 || H <= 0 || N <= 0 || d <= 0 || (dtype != TTT_F32 && dtype != TTT_BF16)) return 0;
+    const size_t U = (size_t)B * H, dd = (size_t)d * d;
+    return align256(U * 2 * dd * 4) + 2 * align256(U * dd * 4) + orth_plan((long long)U, d, d).total;
+}
+
+int ttt_linear_fullbatch_orth(const void* q, const void* k, const void* v, const float* w0, void* out, float* w_star,
+                              int B, int H, int N, int d, float eta, int steps, float a, float b, float c, float eps,
+                              int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("ttt_linear_fullbatch_orth");
+    if (int rc = check_common(q, k, v, out, dtype, eta)) return rc;
+    if (!w0 || !aligned16(w0) || (w_star && !aligned16(w_star))) return TTT_ERR_INVALID_ARG;
+    if (B <= 0 || H <= 0 || N <= 0 || d <= 0) return TTT_ERR_INVALID_ARG;
+    if (int rc = orth_check(steps, a, b, c, eps)) return rc;
+    const long long U = (long long)B * H;
+    if (d > 128 || U > 65535 || !grid_ok(U, (long long)N * d)) return TTT_ERR_UNSUPPORTED;
+    const size_t need = ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dtype);
+    if (workspace_bytes < need || !workspace) return TTT_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TTT_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const long long dd = (long long)d * d;
+    char* w = static_cast<char*>(workspace);
+    float* gc = reinterpret_cast<float*>(w);
+    w += align256((size_t)U * 2 * dd * 4);
+    float* g = reinterpret_cast<float*>(w);
+    w += align256((size_t)U * dd * 4);
+    float* wst = reinterpret_cast<float*>(w);
+    w += align256((size_t)U * dd * 4);
+    auto run = [&](auto t) -> int {
+        using T = decltype(t);
+        simt::linear_gram<T><<<grid_units(U, 2 * dd), simt::TPB, 0, st>>>(static_cast<const T*>(k),
+                                                                         static_cast<const T*>(v), gc, N, d);
+        orth::gradient_kernel<<<grid_units(U, dd), orth::TPB, 0, st>>>(gc, w0, g, H, d, (float)(1.0 / N));
+        if (int rc = orth_run(g, g, U, d, d, steps, a, b, c, eps, 1.f, w, st)) return rc;
+        orth::step_kernel<<<grid_units(U, dd), orth::TPB, 0, st>>>(g, w0, wst, w_star, H, (int)dd, eta);
+        simt::linear_apply<T><<<grid_units(U, (long long)N * d), simt::TPB, 0, st>>>(static_cast<const T*>(q), wst,
+                                                                                    static_cast<T*>(out), N, d);
+        return launched(4);
+    };
+    return dtype == TTT_BF16 ? run(__nv_bfloat16()) : run(float());
+}
 
 }  // extern "C"

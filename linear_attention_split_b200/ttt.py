@@ -95,6 +95,22 @@ def lib():
         L.ttt_linear_chunked_bidir_noalloc.argtypes = [p, p, p, p, p, i, i, i, i, i, f, i, p]
         L.ttt_linear_chunked_bidir_noalloc_max_bytes.restype = sz
         L.ttt_linear_chunked_bidir_noalloc_max_bytes.argtypes = []
+        L.ttt_layernorm.restype = i
+        L.ttt_layernorm.argtypes = [p, p, p, p, i, i, f, i, p]
+        L.ttt_layernorm_bwd_workspace_bytes.restype = sz
+        L.ttt_layernorm_bwd_workspace_bytes.argtypes = [i, i, i]
+        L.ttt_layernorm_bwd.restype = i
+        L.ttt_layernorm_bwd.argtypes = [p, p, p, p, p, p, i, i, f, i, p, sz, p]
+        L.ttt_rope.restype = i
+        L.ttt_rope.argtypes = [p, p, p, p, p, i, p, p, i, i, i, i, i, ctypes.c_double, i, i, p, i, p]
+        L.ttt_orthogonalize_workspace_bytes.restype = sz
+        L.ttt_orthogonalize_workspace_bytes.argtypes = [i, i, i, i]
+        L.ttt_orthogonalize.restype = i
+        L.ttt_orthogonalize.argtypes = [p, p, i, i, i, i, f, f, f, f, f, i, p, sz, p]
+        L.ttt_linear_fullbatch_orth_workspace_bytes.restype = sz
+        L.ttt_linear_fullbatch_orth_workspace_bytes.argtypes = [i, i, i, i, i]
+        L.ttt_linear_fullbatch_orth.restype = i
+        L.ttt_linear_fullbatch_orth.argtypes = [p, p, p, p, p, p, i, i, i, i, f, i, f, f, f, f, i, p, sz, p]
         _lib = L
     return _lib
 
@@ -333,6 +349,175 @@ def ttt_linear_chunked_bidir_noalloc(q, k, v, w0, out, chunk, eta=1.0, stream=No
     return out
 
 
+NS_COEF = (3.4445, -4.7750, 2.0315)  # the usual quintic of the Newton-Schulz steps
+
+
+def _one_device(first, *more):
+    """The tensors' device, which has to be one CUDA device."""
+    dev = first.device
+    for t in more:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must be on one device")
+    if not first.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return dev
+
+
+def _scratch(nbytes, workspace, dev, stream):
+    """The caller's workspace, or one allocated on the stream that uses it."""
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the tensors' device")
+        size = workspace.numel() * workspace.element_size()
+        if size < nbytes:
+            raise ValueError("workspace too small")
+        return workspace, size
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(s):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+
+
+def _call(fn, dev, stream, *args):
+    """Call a C entry point with `dev` current, on `stream` (default: dev's current stream)."""
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream))
+    if rc != 0:
+        raise TTTError(fn.__name__, rc)
+
+
+def _rows(x):
+    """(rows, C) of a tensor [..., C]."""
+    C = x.shape[-1] if x.dim() else 0
+    return (x.numel() // C if C else 0), C
+
+
+def _vector(t, C, name):
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (C,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous fp32 tensor [C]")
+
+
+def ttt_layernorm(x, gamma, beta, y, eps=1e-6, stream=None):
+    """Layer norm over the last axis: x, y [..., C] (y may be x); gamma, beta [C] fp32, beta may be None."""
+    dt = _dtype(x, y)
+    rows, C = _rows(x)
+    if y.shape != x.shape:
+        raise ValueError("x and y must have one shape")
+    _vector(gamma, C, "gamma")
+    _vector(beta, C, "beta")
+    dev = _one_device(x, gamma, beta, y)
+    _call(lib().ttt_layernorm, dev, stream, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), rows, C, eps, dt)
+    return y
+
+
+def ttt_layernorm_bwd_workspace_bytes(rows, C, dtype):
+    return lib().ttt_layernorm_bwd_workspace_bytes(rows, C, dtype)
+
+
+def ttt_layernorm_bwd(dy, x, gamma, dx, dgamma, dbeta=None, eps=1e-6, workspace=None, stream=None):
+    """Gradients of ttt_layernorm: dx [..., C] (may be dy or x), dgamma and dbeta [C] fp32 (dbeta may be None)."""
+    dt = _dtype(dy, x, dx)
+    rows, C = _rows(x)
+    if dy.shape != x.shape or dx.shape != x.shape:
+        raise ValueError("dy, x and dx must have one shape")
+    for t, name in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")):
+        _vector(t, C, name)
+    dev = _one_device(x, dy, gamma, dx, dgamma, dbeta)
+    ws, nbytes = _scratch(ttt_layernorm_bwd_workspace_bytes(rows, C, dt), workspace, dev, stream)
+    _call(lib().ttt_layernorm_bwd, dev, stream, _ptr(dy), _ptr(x), _ptr(gamma), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
+          rows, C, eps, dt, _ptr(ws), nbytes)
+    return dx, dgamma, dbeta
+
+
+def _heads(*ts):
+    """The type of [B, H, N, d] tensors whose features are adjacent (any other strides)."""
+    for t in ts:
+        if t.dtype != ts[0].dtype:
+            raise TypeError("q, k and their outputs must share one dtype")
+        if t.dim() != 4 or t.shape != ts[0].shape:
+            raise ValueError("q, k and their outputs must have one shape [B, H, N, d]")
+        if t.stride(3) != 1 and t.shape[3] != 1:
+            raise ValueError("the features of a head must be adjacent")
+    if ts[0].dtype not in _DT:
+        raise TypeError(f"unsupported dtype {ts[0].dtype}")
+    return _DT[ts[0].dtype]
+
+
+def ttt_rope(q, k, q_out, k_out, dims, grid=None, pos=None, base=10000.0, interleaved=False, inverse=False, stream=None):
+    """Rotary positions: q, k and their outputs [B, H, N, d], any strides with adjacent features (k, k_out may be
+    None; an output may be its own input).  dims: the even widths of the axes' sections.  Either grid, the sizes of
+    the token grid, or pos, fp32 [N, axes] or [B, N, axes].  inverse: turn back, which is the backward pass."""
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if (grid is None) == (pos is None):
+        raise ValueError("give either grid or pos")
+    ts = (q, q_out) if k is None else (q, k, q_out, k_out)
+    dt = _heads(*ts)
+    dev = _one_device(*ts, pos)
+    B, H, N, d = q.shape
+    axes = len(dims)
+    if grid is not None and len(grid) != axes:
+        raise ValueError("grid and dims must have one length")
+    batched = 0
+    if pos is not None:
+        batched = int(pos.dim() == 3)
+        if pos.dtype != torch.float32 or not pos.is_contiguous() or \
+                tuple(pos.shape) != ((B, N, axes) if batched else (N, axes)):
+            raise ValueError("pos must be contiguous fp32 [N, axes] or [B, N, axes]")
+    ints = ctypes.c_int * max(axes, 1)
+    strides = (ctypes.c_longlong * 12)(*q.stride()[:3], *(k if k is not None else q).stride()[:3],
+                                       *q_out.stride()[:3], *(k_out if k is not None else q_out).stride()[:3])
+    _call(lib().ttt_rope, dev, stream, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(pos), batched,
+          ints(*grid) if grid is not None else None, ints(*dims), axes, B, H, N, d, base, int(interleaved),
+          int(inverse), strides, dt)
+    return q_out, k_out
+
+
+def ttt_orthogonalize_workspace_bytes(U, m, n, dtype):
+    return lib().ttt_orthogonalize_workspace_bytes(U, m, n, dtype)
+
+
+def ttt_orthogonalize(x, out, steps=5, coef=NS_COEF, eps=1e-7, scale=1.0, workspace=None, stream=None):
+    """out = scale * the Newton-Schulz steps of each matrix of x [..., m, n] (out may be x)."""
+    dt = _dtype(x, out)
+    if x.dim() < 2 or out.shape != x.shape:
+        raise ValueError("x and out must have one shape [..., m, n]")
+    dev = _one_device(x, out)
+    m, n = x.shape[-2:]
+    U = x.numel() // (m * n) if m * n else 0
+    a, b, c = coef
+    ws, nbytes = _scratch(ttt_orthogonalize_workspace_bytes(U, m, n, dt), workspace, dev, stream)
+    _call(lib().ttt_orthogonalize, dev, stream, _ptr(x), _ptr(out), U, m, n, steps, a, b, c, eps, scale, dt, _ptr(ws),
+          nbytes)
+    return out
+
+
+def ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dtype):
+    return lib().ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dtype)
+
+
+def ttt_linear_fullbatch_orth(q, k, v, w0, out, w_star=None, eta=0.1, steps=5, coef=NS_COEF, eps=1e-7, workspace=None,
+                              stream=None):
+    """TTT-Linear whose inner step goes along the orthogonalised gradient; tensors as for ttt_linear_fullbatch."""
+    dt = _dtype(q, k, v, out)
+    _weights(w0, w_star)
+    if q.dim() != 4 or not q.shape == k.shape == v.shape == out.shape:
+        raise ValueError("q, k, v and out must have one shape [B, H, N, d]")
+    B, H, N, d = q.shape
+    if tuple(w0.shape) != (H, d, d) or (w_star is not None and tuple(w_star.shape) != (B, H, d, d)):
+        raise ValueError("w0 must be [H, d, d] and w_star [B, H, d, d]")
+    dev = _one_device(q, k, v, w0, out, w_star)
+    a, b, c = coef
+    ws, nbytes = _scratch(ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dt), workspace, dev, stream)
+    _call(lib().ttt_linear_fullbatch_orth, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(w0), _ptr(out), _ptr(w_star),
+          B, H, N, d, eta, steps, a, b, c, eps, dt, _ptr(ws), nbytes)
+    return out
+
+
 TTT_FAULT_SKIP_LOAD = 0x1
 
 
@@ -416,3 +601,38 @@ def linear_chunked_bidir(q, k, v, w0, chunk, eta=1.0):
     out = torch.empty_like(q)
     ttt_linear_chunked_bidir(q, k, v, w0, out, chunk, eta)
     return out
+
+
+def layernorm(x, gamma, beta=None, eps=1e-6):
+    return ttt_layernorm(x, gamma, beta, torch.empty_like(x), eps)
+
+
+def layernorm_bwd(dy, x, gamma, eps=1e-6, with_dbeta=True):
+    """(dx, dgamma, dbeta); dbeta is None without with_dbeta."""
+    return ttt_layernorm_bwd(dy, x, gamma, torch.empty_like(x), torch.empty_like(gamma),
+                             torch.empty_like(gamma) if with_dbeta else None, eps)
+
+
+def rope(q, k=None, dims=None, grid=None, pos=None, base=10000.0, interleaved=False, inverse=False):
+    """q and k turned to their positions, each contiguous [B, H, N, d]; without k, q alone."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    ttt_rope(q, k, q_out, k_out, dims, grid, pos, base, interleaved, inverse)
+    return q_out if k is None else (q_out, k_out)
+
+
+def rope_bwd(dq, dk=None, dims=None, grid=None, pos=None, base=10000.0, interleaved=False):
+    """Gradients of q and k from those of rope's outputs: the rotation turned back."""
+    return rope(dq, dk, dims, grid, pos, base, interleaved, inverse=True)
+
+
+def orthogonalize(x, steps=5, coef=NS_COEF, eps=1e-7, scale=1.0):
+    return ttt_orthogonalize(x, torch.empty_like(x), steps, coef, eps, scale)
+
+
+def linear_fullbatch_orth(q, k, v, w0, eta=0.1, steps=5, coef=NS_COEF, eps=1e-7, with_w_star=False):
+    out = torch.empty_like(q)
+    ws = torch.empty((q.shape[0], q.shape[1], q.shape[3], q.shape[3]), dtype=torch.float32,
+                     device=q.device) if with_w_star else None
+    ttt_linear_fullbatch_orth(q, k, v, w0, out, ws, eta, steps, coef, eps)
+    return (out, ws) if with_w_star else out
