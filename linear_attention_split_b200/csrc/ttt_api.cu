@@ -875,22 +875,24 @@ bool orth_coef_ok(double a, double b, double c, int steps) {
     return true;
 }
 struct OrthPlan {
-    int M, N, tall, parts;
-    size_t part, y, z, a, b, total;  // byte offsets of the workspace's parts, and its size
+    int M, N, tall, parts, ldx, lda;
+    size_t part, x, z, a, p, total;  // byte offsets of the workspace's parts, and its size
 };
 OrthPlan orth_plan(long long U, int m, int n) {
     OrthPlan p;
     p.tall = m > n;
     p.M = std::min(m, n);
     p.N = std::max(m, n);
+    p.ldx = (p.N + 7) / 8 * 8;
+    p.lda = (p.M + 7) / 8 * 8;
     const long long mn = (long long)m * n;
     p.parts = (int)std::min<long long>(orth::MAX_PARTS, (mn + 4095) / 4096);
     p.part = 0;
-    p.y = align256((size_t)U * p.parts * 8);
-    p.z = p.y + align256((size_t)U * mn * 4);
-    p.a = p.z + align256((size_t)U * mn * 4);
-    p.b = p.a + align256((size_t)U * p.M * p.M * 4);
-    p.total = p.b + align256((size_t)U * p.M * p.M * 4);
+    p.x = align256((size_t)U * p.parts * 8);
+    p.z = p.x + align256((size_t)U * p.M * p.ldx * 4);
+    p.a = p.z + align256((size_t)U * p.M * p.ldx * 4);
+    p.p = p.a + align256((size_t)U * p.M * p.lda * 4);
+    p.total = p.p + align256((size_t)U * p.M * p.lda * 4);
     return p;
 }
 int orth_check(int steps, float a, float b, float c, float eps) {
@@ -903,24 +905,83 @@ int orth_check(int steps, float a, float b, float c, float eps) {
 template <typename T>
 int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, float b, float c, float eps,
              float scale, void* workspace, cudaStream_t st) {
+    using orth::PParams;
+    DeviceInfo* dev = nullptr;
+    if (int rc = current_device(&dev)) return rc;
     const OrthPlan p = orth_plan(U, m, n);
+    const int tm = (p.M + orth::TM - 1) / orth::TM, tn = (p.N + orth::TM - 1) / orth::TM;
+    if (orth::p_smem_bytes() > dev->smem_optin || tm * tn > 65535) return TTT_ERR_UNSUPPORTED;
     const long long mn = (long long)m * n;
     char* w = static_cast<char*>(workspace);
     double* part = reinterpret_cast<double*>(w + p.part);
-    float *y = reinterpret_cast<float*>(w + p.y), *z = reinterpret_cast<float*>(w + p.z);
-    float *g = reinterpret_cast<float*>(w + p.a), *h = reinterpret_cast<float*>(w + p.b);
-    const dim3 each((unsigned)((mn + orth::TPB - 1) / orth::TPB), (unsigned)U);
-    orth::square_kernel<T><<<dim3((unsigned)p.parts, (unsigned)U), orth::TPB, 0, st>>>(x, part, mn);
-    orth::start_kernel<T><<<each, orth::TPB, 0, st>>>(x, part, y, p.parts, p.M, p.N, p.tall, eps);
-    const dim3 gram((p.M + 63) / 64, (p.M + 63) / 64, (unsigned)U), rect((p.N + 63) / 64, (p.M + 63) / 64, (unsigned)U);
+    __half *X = reinterpret_cast<__half*>(w + p.x), *Z = reinterpret_cast<__half*>(w + p.z);
+    __half *A = reinterpret_cast<__half*>(w + p.a), *P = reinterpret_cast<__half*>(w + p.p);
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUtensorMapDataType f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap xk, xn, zk, zn, ak, pk;  // X and Z by rows of K, and by rows of N; A and P are symmetric
+    if (!tmap_bf16_box(&xk, X, p.ldx, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) ||
+        !tmap_bf16_box(&xn, X, p.ldx, p.M, (int)U * 2, 64, orth::KB, sw, f16) ||
+        !tmap_bf16_box(&zk, Z, p.ldx, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) ||
+        !tmap_bf16_box(&zn, Z, p.ldx, p.M, (int)U * 2, 64, orth::KB, sw, f16) ||
+        !tmap_bf16_box(&ak, A, p.lda, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) ||
+        !tmap_bf16_box(&pk, P, p.lda, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16))
+        return TTT_ERR_CUDA;
+    if (cudaFuncSetAttribute(orth::product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, orth::p_smem_bytes()) !=
+        cudaSuccess)
+        return TTT_ERR_CUDA;
+    if (int rc = launch_pdl(orth::square_kernel<T>, dim3((unsigned)p.parts, (unsigned)U), orth::TPB, 0, st, x, part, mn))
+        return rc;
+    if (int rc = launch_pdl(orth::start_kernel<T>, dim3((p.ldx + 31) / 32, (p.M + 31) / 32, (unsigned)U), 256, 0, st, x,
+                            (const double*)part, X, p.parts, p.M, p.N, p.ldx, p.tall, eps))
+        return rc;
+    auto product = [&](const CUtensorMap& first, const CUtensorMap& second, int tiles, int K, PParams q) {
+        q.kblocks = (K + orth::KB - 1) / orth::KB;
+        q.M = p.M;
+        q.N = p.N;
+        q.tall = p.tall;
+        q.tiles_n = tn;
+        q.ca = a;
+        q.cb = b;
+        q.cc = c;
+        q.scale = scale;
+        // few tiles: split K over a cluster, so that the SMs are filled and every CTA has two blocks
+        int S = 1;
+        while (S < orth::MAX_SPLIT && (long long)tiles * U * S * 2 <= dev->sms && q.kblocks >= 4 * S) S *= 2;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)S, (unsigned)tiles, (unsigned)U);
+        cfg.blockDim = dim3(orth::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = orth::p_smem_bytes();
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = S;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, orth::product_kernel, first, second, q) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+    };
     for (int k = 0; k < steps; ++k) {
-        orth::product_kernel<<<gram, orth::TPB, 0, st>>>(y, y, nullptr, g, p.M, p.M, p.N, 1, 1.f, 0.f);
-        orth::product_kernel<<<gram, orth::TPB, 0, st>>>(g, g, g, h, p.M, p.M, p.M, 1, c, b);
-        orth::product_kernel<<<rect, orth::TPB, 0, st>>>(h, y, y, z, p.M, p.N, p.M, 0, 1.f, a);
-        std::swap(y, z);
+        const bool odd = k & 1, last = k + 1 == steps;
+        const CUtensorMap &yk = odd ? zk : xk, &yn = odd ? zn : xn;
+        PParams q = {};
+        q.kind = orth::GRAM;
+        q.y = A;
+        q.ld = p.lda;
+        if (int rc = product(yk, yk, tm * (tm + 1) / 2, p.N, q)) return rc;
+        q.kind = orth::POLY;
+        q.y = P;
+        q.a = A;
+        if (int rc = product(ak, ak, tm * (tm + 1) / 2, p.M, q)) return rc;
+        q.kind = !last ? orth::NEXT : sizeof(T) == 2 ? orth::OUT_BF16 : orth::OUT_F32;
+        q.y = odd ? X : Z;
+        q.ld = p.ldx;
+        q.out = out;
+        if (int rc = product(pk, yn, tm * tn, p.M, q)) return rc;
     }
-    orth::end_kernel<T><<<each, orth::TPB, 0, st>>>(y, out, p.M, p.N, p.tall, scale);
-    return launched(3 + 3 * steps);
+    return launched(2 + 3 * steps);
 }
 
 }  // namespace
