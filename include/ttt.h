@@ -276,7 +276,7 @@ int ttt_linear_fullbatch_orth(const void* q, const void* k, const void* v, const
  * are good to about 1e-6 of their norm, bf16 ones to their rounding.  Errors: steps outside 1..64,
  * eps <= 0 or a non-finite number is TTT_ERR_INVALID_ARG; coefficients under which a value in
  * [0, 1] leaves [-2, 2] on the way (the iteration would run away), U > 65535 or m, n > 32768 is
- * TTT_ERR_UNSUPPORTED.  The workspace is always needed.
+ * TTT_ERR_UNSUPPORTED.  Matrices of at most 64 by 256 (or 256 by 64) need no workspace.
  * ------------------------------------------------------------------------------------ */
 size_t ttt_orthogonalize_workspace_bytes(int U, int m, int n, int dtype);
 int ttt_orthogonalize(const void* x, void* out, int U, int m, int n, int steps, float a, float b, float c,

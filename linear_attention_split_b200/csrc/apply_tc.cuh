@@ -58,6 +58,9 @@ __global__ void __launch_bounds__(THREADS)
         mbar_expect_tx(&bars->qfull, TILE);  // rows past N are zero-filled and counted
         tma_load_3d(qt, &tm_q, 0, tile * MT, u, &bars->qfull);
     }
+    // Under programmatic dependent launch W is the previous grid's; Q is an input of the whole call,
+    // complete before that grid began.  (Without the attribute this returns at once.)
+    griddep_wait();
     // W (row k = input feature, column n = output feature) -> operand row n, column k, as
     // bf16 hi + lo; consecutive threads take consecutive n, so the reads of W are coalesced
     // (all of a thread's loads are issued before any is used: one L2 round trip)

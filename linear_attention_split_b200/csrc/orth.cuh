@@ -332,33 +332,4 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 1) tc::dealloc(tmem, 128);
 }
 
-// ------------------------------------------------- the TTT-Linear step with such an update ---
-// g[u] = (1/N)(G W0[h] - C) from gc[u] = [G | C]
-__global__ void __launch_bounds__(TPB)
-    gradient_kernel(const float* __restrict__ gc, const float* __restrict__ w0, float* __restrict__ g, int H, int d,
-                    float inv_n) {
-    const long long u = blockIdx.x;
-    const int e = blockIdx.y * TPB + threadIdx.x;
-    if (e >= d * d) return;
-    const int i = e / d, j = e % d;
-    const float* G = gc + u * 2 * d * d + (long long)i * 2 * d;
-    const float* W0 = w0 + (u % H) * d * d;
-    float s = 0.f;
-    for (int m = 0; m < d; ++m) s = fmaf(G[m], W0[m * d + j], s);
-    g[u * d * d + e] = (s - G[d + j]) * inv_n;
-}
-
-// W* = W0[h] - eta U
-__global__ void __launch_bounds__(TPB)
-    step_kernel(const float* __restrict__ upd, const float* __restrict__ w0, float* __restrict__ wst,
-                float* __restrict__ w_star_out, int H, int dd, float eta) {
-    const long long u = blockIdx.x;
-    const int e = blockIdx.y * TPB + threadIdx.x;
-    griddep_wait();
-    if (e >= dd) return;
-    const float w = w0[(u % H) * dd + e] - eta * upd[u * dd + e];
-    wst[u * dd + e] = w;
-    if (w_star_out) w_star_out[u * dd + e] = w;
-}
-
 }  // namespace orth

@@ -28,6 +28,7 @@
 #include "norm.cuh"
 #include "rope.cuh"
 #include "orth.cuh"
+#include "orth_small.cuh"
 
 namespace {
 
@@ -875,6 +876,7 @@ bool orth_coef_ok(double a, double b, double c, int steps) {
     return true;
 }
 struct OrthPlan {
+    bool small;  // one block per matrix, no workspace
     int M, N, tall, parts, ldx, lda;
     size_t part, x, z, a, p, total;  // byte offsets of the workspace's parts, and its size
 };
@@ -883,6 +885,7 @@ OrthPlan orth_plan(long long U, int m, int n) {
     p.tall = m > n;
     p.M = std::min(m, n);
     p.N = std::max(m, n);
+    p.small = p.M <= orth::SM_M && p.N <= orth::SM_N;
     p.ldx = (p.N + 7) / 8 * 8;
     p.lda = (p.M + 7) / 8 * 8;
     const long long mn = (long long)m * n;
@@ -892,7 +895,7 @@ OrthPlan orth_plan(long long U, int m, int n) {
     p.z = p.x + align256((size_t)U * p.M * p.ldx * 4);
     p.a = p.z + align256((size_t)U * p.M * p.ldx * 4);
     p.p = p.a + align256((size_t)U * p.M * p.lda * 4);
-    p.total = p.p + align256((size_t)U * p.M * p.lda * 4);
+    p.total = p.small ? 0 : p.p + align256((size_t)U * p.M * p.lda * 4);
     return p;
 }
 int orth_check(int steps, float a, float b, float c, float eps) {
@@ -909,6 +912,16 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
     DeviceInfo* dev = nullptr;
     if (int rc = current_device(&dev)) return rc;
     const OrthPlan p = orth_plan(U, m, n);
+    if (p.small) {
+        const int smem = orth::small_smem_bytes(p.N);
+        if (smem > dev->smem_optin) return TTT_ERR_UNSUPPORTED;
+        if (cudaFuncSetAttribute(orth::small_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return TTT_ERR_CUDA;
+        if (int rc = launch_pdl(orth::small_kernel<T>, dim3((unsigned)U), orth::SM_TPB, smem, st, x, out, p.M, p.N, p.tall,
+                                steps, a, b, c, eps, scale))
+            return rc;
+        return launched(1);
+    }
     const int tm = (p.M + orth::TM - 1) / orth::TM, tn = (p.N + orth::TM - 1) / orth::TM;
     if (orth::p_smem_bytes() > dev->smem_optin || tm * tn > 65535) return TTT_ERR_UNSUPPORTED;
     const long long mn = (long long)m * n;
@@ -982,6 +995,99 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         if (int rc = product(pk, yn, tm * tn, p.M, q)) return rc;
     }
     return launched(2 + 3 * steps);
+}
+
+// ------------------------------------------------------------------ TTT-Linear, orthogonalised step
+struct LinOrthPlan {
+    bool tc;                       // bf16, d = 64: tensor-core sums and output pass
+    int S, TT, n_tiles;            // token splits of a unit; tiles of TT tokens (tc)
+    size_t part, w, g, ns, total;  // byte offsets of the workspace's parts, and its size
+};
+LinOrthPlan lin_orth_plan(long long U, int N, int d, int dtype) {
+    LinOrthPlan p = {};
+    DeviceInfo* dev = nullptr;
+    const int sms = current_device(&dev) == TTT_OK ? dev->sms : 148;
+    p.tc = dtype == TTT_BF16 && d == orth::D;
+    if (p.tc) {
+        const BwdPlan b = bwd_plan(U, N, sms);
+        p.S = b.S;
+        p.TT = b.TT;
+        p.n_tiles = b.n_tiles;
+    } else {  // blocks of at least 64 tokens, about four per SM
+        const int nb = (d + 63) / 64;
+        p.S = 1;
+        while (p.S < 16 && U * p.S * 2 * nb * nb < 4LL * sms && N >= 128 * p.S) p.S *= 2;
+    }
+    const size_t dd = (size_t)d * d;
+    p.part = 0;
+    p.w = align256((size_t)U * p.S * 2 * dd * 4);
+    p.g = p.w + align256((size_t)U * dd * 4);
+    p.ns = p.g + (d > orth::SM_M ? align256((size_t)U * dd * 4) : 0);
+    p.total = p.ns + (d > orth::SM_M ? orth_plan(U, d, d).total : 0);
+    return p;
+}
+// W* goes straight to w_star where the caller wants it
+template <typename T>
+int lin_orth(const void* q, const void* k, const void* v, const float* w0, void* out, float* w_star, long long U, int H, int N,
+             int d, float eta, int steps, float a, float b, float c, float eps, void* workspace, cudaStream_t st) {
+    DeviceInfo* dev = nullptr;
+    if (int rc = current_device(&dev)) return rc;
+    const LinOrthPlan p = lin_orth_plan(U, N, d, sizeof(T) == 2 ? TTT_BF16 : TTT_F32);
+    char* ws = static_cast<char*>(workspace);
+    float* part = reinterpret_cast<float*>(ws + p.part);
+    float* w = w_star ? w_star : reinterpret_cast<float*>(ws + p.w);
+    const float inv_n = (float)(1.0 / N);
+    const int nb = (d + 63) / 64;
+    if (p.tc) {
+        CUtensorMap tk, tv;
+        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+        if (!tmap_bf16_3d(&tk, k, 64, N, (int)U, p.TT, sw) || !tmap_bf16_3d(&tv, v, 64, N, (int)U, p.TT, sw)) return TTT_ERR_CUDA;
+        if (cudaFuncSetAttribute(orth::gram_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, orth::g_smem_bytes()) !=
+            cudaSuccess)
+            return TTT_ERR_CUDA;
+        if (int rc = launch_pdl(orth::gram_tc_kernel, dim3((unsigned)p.S, (unsigned)U), orth::THREADS, orth::g_smem_bytes(), st, tv,
+                                tk, part, p.TT, p.n_tiles))
+            return rc;
+    } else {
+        if (int rc = launch_pdl(orth::gram_kernel<T>, dim3((unsigned)p.S, (unsigned)U, 2 * nb * nb), 256, 0, st,
+                                static_cast<const T*>(k), static_cast<const T*>(v), part, N, d))
+            return rc;
+    }
+    if (d <= orth::SM_M) {
+        const int smem = orth::update_smem_bytes();
+        if (cudaFuncSetAttribute(orth::update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return TTT_ERR_CUDA;
+        if (int rc = launch_pdl(orth::update_kernel, dim3((unsigned)U), orth::SM_TPB, smem, st, (const float*)part, w0, w, p.S, H, d,
+                                inv_n, eta, steps, a, b, c, eps))
+            return rc;
+        launched(2);
+    } else {
+        float* g = reinterpret_cast<float*>(ws + p.g);
+        if (int rc = launch_pdl(orth::gradient_kernel, grid_units(U, (long long)d * d), orth::TPB, 0, st, (const float*)part, w0, g,
+                                p.S, H, d, inv_n))
+            return rc;
+        if (int rc = orth_run<float>(g, g, U, d, d, steps, a, b, c, eps, 1.f, ws + p.ns, st)) return rc;
+        if (int rc = launch_pdl(orth::step_kernel, grid_units(U, (long long)d * d), orth::TPB, 0, st, (const float*)g, w0, w, H,
+                                d * d, eta))
+            return rc;
+        launched(3);
+    }
+    if (p.tc) {
+        CUtensorMap tq, to;
+        if (!tmap_bf16_3d(&tq, q, atc::D, N, (int)U, atc::MT, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !tmap_bf16_3d(&to, out, atc::D, N, (int)U, atc::MT, CU_TENSOR_MAP_SWIZZLE_128B))
+            return TTT_ERR_CUDA;
+        if (cudaFuncSetAttribute(atc::apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, atc::smem_bytes()) != cudaSuccess)
+            return TTT_ERR_CUDA;
+        if (int rc = launch_pdl(atc::apply_kernel, dim3((unsigned)((N + atc::MT - 1) / atc::MT), (unsigned)U), atc::THREADS,
+                                atc::smem_bytes(), st, tq, to, (const float*)w))
+            return rc;
+    } else {
+        if (int rc = launch_pdl(orth::apply_kernel<T>, dim3((unsigned)((N + 63) / 64), (unsigned)U, nb), 256, 0, st,
+                                static_cast<const T*>(q), (const float*)w, static_cast<T*>(out), N, d))
+            return rc;
+    }
+    return launched(1);
 }
 
 }  // namespace
@@ -1598,8 +1704,8 @@ int ttt_orthogonalize(const void* x, void* out, int U, int m, int n, int steps, 
     if (int rc = orth_check(steps, a, b, c, eps)) return rc;
     if (U > 65535 || m > 32768 || n > 32768) return TTT_ERR_UNSUPPORTED;
     const size_t need = ttt_orthogonalize_workspace_bytes(U, m, n, dtype);
-    if (workspace_bytes < need || !workspace) return TTT_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return TTT_ERR_INVALID_ARG;
+    if (workspace_bytes < need || (need && !workspace)) return TTT_ERR_WORKSPACE;
+    if (workspace && !aligned16(workspace)) return TTT_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == TTT_BF16)
         return orth_run(static_cast<const __nv_bfloat16*>(x), static_cast<__nv_bfloat16*>(out), U, m, n, steps, a, b, c,
@@ -1611,8 +1717,7 @@ int ttt_orthogonalize(const void* x, void* out, int U, int m, int n, int steps, 
 // ------------------------------------------------------------------ TTT-Linear, orthogonalised step
 size_t ttt_linear_fullbatch_orth_workspace_bytes(int B, int H, int N, int d, int dtype) {
     if (B <= 0 || H <= 0 || N <= 0 || d <= 0 || (dtype != TTT_F32 && dtype != TTT_BF16)) return 0;
-    const size_t U = (size_t)B * H, dd = (size_t)d * d;
-    return align256(U * 2 * dd * 4) + 2 * align256(U * dd * 4) + orth_plan((long long)U, d, d).total;
+    return lin_orth_plan((long long)B * H, N, d, dtype).total;
 }
 
 int ttt_linear_fullbatch_orth(const void* q, const void* k, const void* v, const float* w0, void* out, float* w_star,
@@ -1624,31 +1729,14 @@ int ttt_linear_fullbatch_orth(const void* q, const void* k, const void* v, const
     if (B <= 0 || H <= 0 || N <= 0 || d <= 0) return TTT_ERR_INVALID_ARG;
     if (int rc = orth_check(steps, a, b, c, eps)) return rc;
     const long long U = (long long)B * H;
-    if (d > 128 || U > 65535 || !grid_ok(U, (long long)N * d)) return TTT_ERR_UNSUPPORTED;
+    if (d > 128 || U > 65535) return TTT_ERR_UNSUPPORTED;
     const size_t need = ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dtype);
     if (workspace_bytes < need || !workspace) return TTT_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TTT_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const long long dd = (long long)d * d;
-    char* w = static_cast<char*>(workspace);
-    float* gc = reinterpret_cast<float*>(w);
-    w += align256((size_t)U * 2 * dd * 4);
-    float* g = reinterpret_cast<float*>(w);
-    w += align256((size_t)U * dd * 4);
-    float* wst = reinterpret_cast<float*>(w);
-    w += align256((size_t)U * dd * 4);
-    auto run = [&](auto t) -> int {
-        using T = decltype(t);
-        simt::linear_gram<T><<<grid_units(U, 2 * dd), simt::TPB, 0, st>>>(static_cast<const T*>(k),
-                                                                         static_cast<const T*>(v), gc, N, d);
-        orth::gradient_kernel<<<grid_units(U, dd), orth::TPB, 0, st>>>(gc, w0, g, H, d, (float)(1.0 / N));
-        if (int rc = orth_run(g, g, U, d, d, steps, a, b, c, eps, 1.f, w, st)) return rc;
-        orth::step_kernel<<<grid_units(U, dd), orth::TPB, 0, st>>>(g, w0, wst, w_star, H, (int)dd, eta);
-        simt::linear_apply<T><<<grid_units(U, (long long)N * d), simt::TPB, 0, st>>>(static_cast<const T*>(q), wst,
-                                                                                    static_cast<T*>(out), N, d);
-        return launched(4);
-    };
-    return dtype == TTT_BF16 ? run(__nv_bfloat16()) : run(float());
+    if (dtype == TTT_BF16)
+        return lin_orth<__nv_bfloat16>(q, k, v, w0, out, w_star, U, H, N, d, eta, steps, a, b, c, eps, workspace, st);
+    return lin_orth<float>(q, k, v, w0, out, w_star, U, H, N, d, eta, steps, a, b, c, eps, workspace, st);
 }
 
 }  // extern "C"

@@ -372,6 +372,8 @@ def _scratch(nbytes, workspace, dev, stream):
         if size < nbytes:
             raise ValueError("workspace too small")
         return workspace, size
+    if nbytes == 0:
+        return None, 0
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)

@@ -89,7 +89,7 @@ def orth(L, x=FAKE, out=FAKE, U=1, m=8, n=8, steps=5, coef=ttt.NS_COEF, eps=1e-7
     (dict(scale=INF), INVALID), (dict(coef=(NAN, 0.0, 0.0)), INVALID), (dict(dt=5), INVALID),
     (dict(coef=(4.0, 0.0, 0.0)), UNSUPPORTED), (dict(coef=(3.4445, 4.775, 2.0315)), UNSUPPORTED),
     (dict(coef=(2.0, -40.0, 39.0)), UNSUPPORTED), (dict(U=65536), UNSUPPORTED), (dict(m=32769), UNSUPPORTED),
-    (dict(ws=None), WORKSPACE), (dict(nb=16), WORKSPACE), (dict(ws=MISALIGNED), INVALID)])
+    (dict(ws=None, m=80, n=80), WORKSPACE), (dict(nb=16, n=257), WORKSPACE), (dict(ws=MISALIGNED), INVALID)])
 def test_orthogonalize_refusals(L, change, want):
     assert orth(L, **change) == want
 
@@ -110,7 +110,9 @@ def test_workspace_queries(L):
     assert L.ttt_layernorm_bwd_workspace_bytes(0, 64, 1) == 0
     assert L.ttt_layernorm_bwd_workspace_bytes(1, 64, 1) >= 2 * 64 * 4
     assert L.ttt_orthogonalize_workspace_bytes(1, 0, 4, 0) == 0
-    assert L.ttt_orthogonalize_workspace_bytes(1, 64, 64, 0) > 0
+    assert L.ttt_orthogonalize_workspace_bytes(3, 64, 256, 0) == 0  # a block's shared memory holds it
+    assert L.ttt_orthogonalize_workspace_bytes(1, 65, 65, 0) > 0
+    assert L.ttt_orthogonalize_workspace_bytes(1, 257, 64, 1) > 0
     assert L.ttt_linear_fullbatch_orth_workspace_bytes(1, 1, 16, 64, 1) > 0
 
 
