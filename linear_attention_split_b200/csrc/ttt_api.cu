@@ -71,6 +71,22 @@ int current_device(DeviceInfo** info) {
     return TTT_OK;
 }
 
+// Lets a kernel use `bytes` of dynamic shared memory; asked of the driver once per kernel and device
+// (`done` is the kernel's own record; `bytes` is the most the kernel ever takes, so that calls of
+// several threads agree).
+struct SmemRecord {
+    std::atomic<int> bytes[kMaxDevices] = {};
+};
+template <typename Kern>
+bool allow_smem(Kern kern, int bytes, SmemRecord& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    if (done.bytes[dev].load(std::memory_order_acquire) >= bytes) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.bytes[dev].store(bytes, std::memory_order_release);
+    return true;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int launched(int n) {
@@ -862,13 +878,21 @@ bool rope_strides_disjoint(const long long* st, int B, int H, int N, int d) {
 // Whether the iteration stays bounded: every value in [0, 1] (the singular values of a matrix of
 // Frobenius norm 1) keeps to at most 2 through all steps, and |b s^2| + |c s^4| to at most 32.
 bool orth_coef_ok(double a, double b, double c, int steps) {
-    double top = 1.0;
+    double top = 1.0;  // the values reach from 0 to here
+    const auto p = [&](double t) { return std::fabs(std::sqrt(t) * (a + t * (b + t * c))); };  // of t = s^2
     for (int k = 0; k < steps; ++k) {
-        if (std::fabs(b) * top * top + std::fabs(c) * top * top * top * top > 32.0) return false;
-        double next = 0.0;
-        for (int i = 0; i <= 2048; ++i) {
-            const double s = top * i / 2048.0;
-            next = std::max(next, std::fabs(s * (a + s * s * (b + c * s * s))));
+        const double t = top * top;
+        if (std::fabs(b) * t + std::fabs(c) * t * t > 32.0) return false;
+        double next = p(t);
+        // extremes inside: p'(s) = a + 3 b s^2 + 5 c s^4 = 0
+        const double root = 9.0 * b * b - 20.0 * a * c;
+        if (c == 0.0) {
+            if (b != 0.0 && -a / (3.0 * b) > 0.0 && -a / (3.0 * b) < t) next = std::max(next, p(-a / (3.0 * b)));
+        } else if (root >= 0.0) {
+            for (const double sign : {-1.0, 1.0}) {
+                const double at = (-3.0 * b + sign * std::sqrt(root)) / (10.0 * c);
+                if (at > 0.0 && at < t) next = std::max(next, p(at));
+            }
         }
         if (!(next <= 2.0)) return false;
         top = next;
@@ -914,9 +938,9 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
     const OrthPlan p = orth_plan(U, m, n);
     if (p.small) {
         const int smem = orth::small_smem_bytes(p.N);
-        if (smem > dev->smem_optin) return TTT_ERR_UNSUPPORTED;
-        if (cudaFuncSetAttribute(orth::small_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return TTT_ERR_CUDA;
+        if (orth::small_smem_bytes(orth::SM_N) > dev->smem_optin) return TTT_ERR_UNSUPPORTED;
+        static SmemRecord record;
+        if (!allow_smem(orth::small_kernel<T>, orth::small_smem_bytes(orth::SM_N), record)) return TTT_ERR_CUDA;
         if (int rc = launch_pdl(orth::small_kernel<T>, dim3((unsigned)U), orth::SM_TPB, smem, st, x, out, p.M, p.N, p.tall,
                                 steps, a, b, c, eps, scale))
             return rc;
@@ -939,9 +963,8 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         !tmap_bf16_box(&ak, A, p.lda, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) ||
         !tmap_bf16_box(&pk, P, p.lda, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16))
         return TTT_ERR_CUDA;
-    if (cudaFuncSetAttribute(orth::product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, orth::p_smem_bytes()) !=
-        cudaSuccess)
-        return TTT_ERR_CUDA;
+    static SmemRecord record;
+    if (!allow_smem(orth::product_kernel, orth::p_smem_bytes(), record)) return TTT_ERR_CUDA;
     if (int rc = launch_pdl(orth::square_kernel<T>, dim3((unsigned)p.parts, (unsigned)U), orth::TPB, 0, st, x, part, mn))
         return rc;
     if (int rc = launch_pdl(orth::start_kernel<T>, dim3((p.ldx + 31) / 32, (p.M + 31) / 32, (unsigned)U), 256, 0, st, x,
@@ -1042,9 +1065,8 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
         CUtensorMap tk, tv;
         const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
         if (!tmap_bf16_3d(&tk, k, 64, N, (int)U, p.TT, sw) || !tmap_bf16_3d(&tv, v, 64, N, (int)U, p.TT, sw)) return TTT_ERR_CUDA;
-        if (cudaFuncSetAttribute(orth::gram_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, orth::g_smem_bytes()) !=
-            cudaSuccess)
-            return TTT_ERR_CUDA;
+        static SmemRecord record;
+        if (!allow_smem(orth::gram_tc_kernel, orth::g_smem_bytes(), record)) return TTT_ERR_CUDA;
         if (int rc = launch_pdl(orth::gram_tc_kernel, dim3((unsigned)p.S, (unsigned)U), orth::THREADS, orth::g_smem_bytes(), st, tv,
                                 tk, part, p.TT, p.n_tiles))
             return rc;
@@ -1055,8 +1077,8 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
     }
     if (d <= orth::SM_M) {
         const int smem = orth::update_smem_bytes();
-        if (cudaFuncSetAttribute(orth::update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return TTT_ERR_CUDA;
+        static SmemRecord record;
+        if (!allow_smem(orth::update_kernel, smem, record)) return TTT_ERR_CUDA;
         if (int rc = launch_pdl(orth::update_kernel, dim3((unsigned)U), orth::SM_TPB, smem, st, (const float*)part, w0, w, p.S, H, d,
                                 inv_n, eta, steps, a, b, c, eps))
             return rc;
@@ -1077,8 +1099,8 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
         if (!tmap_bf16_3d(&tq, q, atc::D, N, (int)U, atc::MT, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !tmap_bf16_3d(&to, out, atc::D, N, (int)U, atc::MT, CU_TENSOR_MAP_SWIZZLE_128B))
             return TTT_ERR_CUDA;
-        if (cudaFuncSetAttribute(atc::apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, atc::smem_bytes()) != cudaSuccess)
-            return TTT_ERR_CUDA;
+        static SmemRecord record;
+        if (!allow_smem(atc::apply_kernel, atc::smem_bytes(), record)) return TTT_ERR_CUDA;
         if (int rc = launch_pdl(atc::apply_kernel, dim3((unsigned)((N + atc::MT - 1) / atc::MT), (unsigned)U), atc::THREADS,
                                 atc::smem_bytes(), st, tq, to, (const float*)w))
             return rc;

@@ -8,6 +8,7 @@ been built this module raises on first use -- there is no fallback implementatio
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -353,43 +354,60 @@ NS_COEF = (3.4445, -4.7750, 2.0315)  # the usual quintic of the Newton-Schulz st
 
 
 def _one_device(first, *more):
-    """The tensors' device, which has to be one CUDA device."""
-    dev = first.device
+    """The index of the tensors' device, which has to be one CUDA device."""
+    dev = first.get_device()
     for t in more:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors must be on one device")
-    if not first.is_cuda:
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
     return dev
 
 
+@functools.lru_cache(maxsize=512)
+def _scratch_bytes(query, dev, *args):
+    """A workspace query's answer, kept by its arguments and the device whose SM count it may go by."""
+    with torch.cuda.device(dev):
+        return getattr(lib(), query)(*args)
+
+
 def _scratch(nbytes, workspace, dev, stream):
-    """The caller's workspace, or one allocated on the stream that uses it."""
+    """(pointer, size, owner) of the caller's workspace, or of one allocated on the stream that uses it."""
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("the workspace must be contiguous and on the tensors' device")
         size = workspace.numel() * workspace.element_size()
         if size < nbytes:
             raise ValueError("workspace too small")
-        return workspace, size
+        return workspace.data_ptr() or None, size, workspace
     if nbytes == 0:
-        return None, 0
+        return None, 0, None
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(s):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
+        with torch.cuda.stream(s):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ws.data_ptr(), nbytes, ws
 
 
 def _call(fn, dev, stream, *args):
     """Call a C entry point with `dev` current, on `stream` (default: dev's current stream)."""
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(stream))
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, st)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream))
+            rc = fn(*args, st)
     if rc != 0:
         raise TTTError(fn.__name__, rc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rows(x):
@@ -412,7 +430,7 @@ def ttt_layernorm(x, gamma, beta, y, eps=1e-6, stream=None):
     _vector(gamma, C, "gamma")
     _vector(beta, C, "beta")
     dev = _one_device(x, gamma, beta, y)
-    _call(lib().ttt_layernorm, dev, stream, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), rows, C, eps, dt)
+    _call(lib().ttt_layernorm, dev, stream, _at(x), _at(gamma), _at(beta), _at(y), rows, C, eps, dt)
     return y
 
 
@@ -429,24 +447,23 @@ def ttt_layernorm_bwd(dy, x, gamma, dx, dgamma, dbeta=None, eps=1e-6, workspace=
     for t, name in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")):
         _vector(t, C, name)
     dev = _one_device(x, dy, gamma, dx, dgamma, dbeta)
-    ws, nbytes = _scratch(ttt_layernorm_bwd_workspace_bytes(rows, C, dt), workspace, dev, stream)
-    _call(lib().ttt_layernorm_bwd, dev, stream, _ptr(dy), _ptr(x), _ptr(gamma), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
-          rows, C, eps, dt, _ptr(ws), nbytes)
+    ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_layernorm_bwd_workspace_bytes", dev, rows, C, dt), workspace, dev, stream)
+    _call(lib().ttt_layernorm_bwd, dev, stream, _at(dy), _at(x), _at(gamma), _at(dx), _at(dgamma), _at(dbeta),
+          rows, C, eps, dt, ws, nbytes)
     return dx, dgamma, dbeta
 
 
-def _heads(*ts):
-    """The type of [B, H, N, d] tensors whose features are adjacent (any other strides)."""
-    for t in ts:
-        if t.dtype != ts[0].dtype:
-            raise TypeError("q, k and their outputs must share one dtype")
-        if t.dim() != 4 or t.shape != ts[0].shape:
-            raise ValueError("q, k and their outputs must have one shape [B, H, N, d]")
-        if t.stride(3) != 1 and t.shape[3] != 1:
-            raise ValueError("the features of a head must be adjacent")
-    if ts[0].dtype not in _DT:
-        raise TypeError(f"unsupported dtype {ts[0].dtype}")
-    return _DT[ts[0].dtype]
+@functools.lru_cache(maxsize=256)
+def _ints(*values):
+    """A host array of int that the library reads (kept by its values)."""
+    return (ctypes.c_int * max(len(values), 1))(*values)
+
+
+@functools.lru_cache(maxsize=256)
+def _strides(*tensors):
+    """The host array of (b, h, n) strides of the tensors, from their stride tuples; a missing one is zeros."""
+    flat = [v for t in tensors for v in (t[:3] if t else (0, 0, 0))]
+    return (ctypes.c_longlong * len(flat))(*flat)
 
 
 def ttt_rope(q, k, q_out, k_out, dims, grid=None, pos=None, base=10000.0, interleaved=False, inverse=False, stream=None):
@@ -457,10 +474,25 @@ def ttt_rope(q, k, q_out, k_out, dims, grid=None, pos=None, base=10000.0, interl
         raise ValueError("k and k_out go together")
     if (grid is None) == (pos is None):
         raise ValueError("give either grid or pos")
-    ts = (q, q_out) if k is None else (q, k, q_out, k_out)
-    dt = _heads(*ts)
-    dev = _one_device(*ts, pos)
-    B, H, N, d = q.shape
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 4:
+        raise ValueError("q, k and their outputs must be [B, H, N, d]")
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    B, H, N, d = shape
+    st = []
+    for t in (q, k, q_out, k_out):
+        if t is None:
+            st.append(None)
+            continue
+        if t.dtype != dtype:
+            raise TypeError("q, k and their outputs must share one dtype")
+        if t.shape != shape:
+            raise ValueError("q, k and their outputs must have one shape")
+        st.append(t.stride())
+        if st[-1][3] != 1 and d != 1:
+            raise ValueError("the features of a head must be adjacent")
+    dev = _one_device(q, k, q_out, k_out, pos)
     axes = len(dims)
     if grid is not None and len(grid) != axes:
         raise ValueError("grid and dims must have one length")
@@ -470,12 +502,9 @@ def ttt_rope(q, k, q_out, k_out, dims, grid=None, pos=None, base=10000.0, interl
         if pos.dtype != torch.float32 or not pos.is_contiguous() or \
                 tuple(pos.shape) != ((B, N, axes) if batched else (N, axes)):
             raise ValueError("pos must be contiguous fp32 [N, axes] or [B, N, axes]")
-    ints = ctypes.c_int * max(axes, 1)
-    strides = (ctypes.c_longlong * 12)(*q.stride()[:3], *(k if k is not None else q).stride()[:3],
-                                       *q_out.stride()[:3], *(k_out if k is not None else q_out).stride()[:3])
-    _call(lib().ttt_rope, dev, stream, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(pos), batched,
-          ints(*grid) if grid is not None else None, ints(*dims), axes, B, H, N, d, base, int(interleaved),
-          int(inverse), strides, dt)
+    _call(lib().ttt_rope, dev, stream, q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), _at(pos), batched,
+          _ints(*grid) if grid is not None else None, _ints(*dims), axes, B, H, N, d, base, interleaved, inverse,
+          _strides(*st), _DT[dtype])
     return q_out, k_out
 
 
@@ -492,8 +521,8 @@ def ttt_orthogonalize(x, out, steps=5, coef=NS_COEF, eps=1e-7, scale=1.0, worksp
     m, n = x.shape[-2:]
     U = x.numel() // (m * n) if m * n else 0
     a, b, c = coef
-    ws, nbytes = _scratch(ttt_orthogonalize_workspace_bytes(U, m, n, dt), workspace, dev, stream)
-    _call(lib().ttt_orthogonalize, dev, stream, _ptr(x), _ptr(out), U, m, n, steps, a, b, c, eps, scale, dt, _ptr(ws),
+    ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_orthogonalize_workspace_bytes", dev, U, m, n, dt), workspace, dev, stream)
+    _call(lib().ttt_orthogonalize, dev, stream, _at(x), _at(out), U, m, n, steps, a, b, c, eps, scale, dt, ws,
           nbytes)
     return out
 
@@ -514,9 +543,9 @@ def ttt_linear_fullbatch_orth(q, k, v, w0, out, w_star=None, eta=0.1, steps=5, c
         raise ValueError("w0 must be [H, d, d] and w_star [B, H, d, d]")
     dev = _one_device(q, k, v, w0, out, w_star)
     a, b, c = coef
-    ws, nbytes = _scratch(ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dt), workspace, dev, stream)
-    _call(lib().ttt_linear_fullbatch_orth, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(w0), _ptr(out), _ptr(w_star),
-          B, H, N, d, eta, steps, a, b, c, eps, dt, _ptr(ws), nbytes)
+    ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_linear_fullbatch_orth_workspace_bytes", dev, B, H, N, d, dt), workspace, dev, stream)
+    _call(lib().ttt_linear_fullbatch_orth, dev, stream, _at(q), _at(k), _at(v), _at(w0), _at(out), _at(w_star),
+          B, H, N, d, eta, steps, a, b, c, eps, dt, ws, nbytes)
     return out
 
 
@@ -617,8 +646,8 @@ def layernorm_bwd(dy, x, gamma, eps=1e-6, with_dbeta=True):
 
 def rope(q, k=None, dims=None, grid=None, pos=None, base=10000.0, interleaved=False, inverse=False):
     """q and k turned to their positions, each contiguous [B, H, N, d]; without k, q alone."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
     ttt_rope(q, k, q_out, k_out, dims, grid, pos, base, interleaved, inverse)
     return q_out if k is None else (q_out, k_out)
 
