@@ -902,7 +902,7 @@ bool orth_coef_ok(double a, double b, double c, int steps) {
 struct OrthPlan {
     bool small;  // one block per matrix, no workspace
     int M, N, tall, parts, ldx, lda;
-    size_t part, x, z, a, p, total;  // byte offsets of the workspace's parts, and its size
+    size_t part, x, z, a, q, p, total;  // byte offsets of the workspace's parts, and its size
 };
 OrthPlan orth_plan(long long U, int m, int n) {
     OrthPlan p;
@@ -918,7 +918,8 @@ OrthPlan orth_plan(long long U, int m, int n) {
     p.x = align256((size_t)U * p.parts * 8);
     p.z = p.x + align256((size_t)U * p.M * p.ldx * 4);
     p.a = p.z + align256((size_t)U * p.M * p.ldx * 4);
-    p.p = p.a + align256((size_t)U * p.M * p.lda * 4);
+    p.q = p.a + align256((size_t)U * p.M * p.lda * 4);
+    p.p = p.q + align256((size_t)U * p.M * p.lda * 4);
     p.total = p.small ? 0 : p.p + align256((size_t)U * p.M * p.lda * 4);
     return p;
 }
@@ -947,30 +948,44 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         return launched(1);
     }
     const int tm = (p.M + orth::TM - 1) / orth::TM, tn = (p.N + orth::TM - 1) / orth::TM;
-    if (orth::p_smem_bytes() > dev->smem_optin || tm * tn > 65535) return TTT_ERR_UNSUPPORTED;
+    if (orth::Full::SMEM > dev->smem_optin || tm * tn > 65535) return TTT_ERR_UNSUPPORTED;
     const long long mn = (long long)m * n;
     char* w = static_cast<char*>(workspace);
     double* part = reinterpret_cast<double*>(w + p.part);
     __half *X = reinterpret_cast<__half*>(w + p.x), *Z = reinterpret_cast<__half*>(w + p.z);
-    __half *A = reinterpret_cast<__half*>(w + p.a), *P = reinterpret_cast<__half*>(w + p.p);
-    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    const CUtensorMapDataType f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap xk, xn, zk, zn, ak, pk;  // X and Z by rows of K, and by rows of N; A and P are symmetric
-    if (!tmap_bf16_box(&xk, X, p.ldx, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) ||
-        !tmap_bf16_box(&xn, X, p.ldx, p.M, (int)U * 2, 64, orth::KB, sw, f16) ||
-        !tmap_bf16_box(&zk, Z, p.ldx, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) ||
-        !tmap_bf16_box(&zn, Z, p.ldx, p.M, (int)U * 2, 64, orth::KB, sw, f16) ||
-        !tmap_bf16_box(&ak, A, p.lda, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) ||
-        !tmap_bf16_box(&pk, P, p.lda, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16))
+    __half *A = reinterpret_cast<__half*>(w + p.a), *Q = reinterpret_cast<__half*>(w + p.q), *P = reinterpret_cast<__half*>(w + p.p);
+    auto maps = [&](__half* y, int ld, CUtensorMap* k, CUtensorMap* mn_map) {
+        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+        const CUtensorMapDataType f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        return tmap_bf16_box(k, y, ld, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) &&
+               tmap_bf16_box(mn_map, y, ld, p.M, (int)U * 2, 64, orth::KB, sw, f16);
+    };
+    orth::Maps gram[2], poly, next[2];  // [1]: X is in Z
+    for (int t = 0; t < 2; ++t) {
+        if (!maps(t ? Z : X, p.ldx, &gram[t].first_k, &gram[t].first_mn)) return TTT_ERR_CUDA;
+        gram[t].second_k = next[t].second_k = gram[t].first_k;
+        gram[t].second_mn = next[t].second_mn = gram[t].first_mn;
+    }
+    if (!maps(A, p.lda, &poly.first_k, &poly.first_mn) || !maps(Q, p.lda, &poly.second_k, &poly.second_mn) ||
+        !maps(P, p.lda, &next[0].first_k, &next[0].first_mn))
         return TTT_ERR_CUDA;
-    static SmemRecord record;
-    if (!allow_smem(orth::product_kernel, orth::p_smem_bytes(), record)) return TTT_ERR_CUDA;
+    next[1].first_k = next[0].first_k;
+    next[1].first_mn = next[0].first_mn;
+    constexpr bool kHalf = sizeof(T) == 2;  // bf16: X is held in one fp16 number
+    using GramC = std::conditional_t<kHalf, orth::High, orth::Full>;
+    using NextC = std::conditional_t<kHalf, orth::Left, orth::Full>;
+    static SmemRecord gram_smem, poly_smem, next_smem;
+    if (!allow_smem(orth::product_kernel<GramC>, GramC::SMEM, gram_smem) ||
+        !allow_smem(orth::product_kernel<orth::Full>, orth::Full::SMEM, poly_smem) ||
+        !allow_smem(orth::product_kernel<NextC>, NextC::SMEM, next_smem))
+        return TTT_ERR_CUDA;
     if (int rc = launch_pdl(orth::square_kernel<T>, dim3((unsigned)p.parts, (unsigned)U), orth::TPB, 0, st, x, part, mn))
         return rc;
     if (int rc = launch_pdl(orth::start_kernel<T>, dim3((p.ldx + 31) / 32, (p.M + 31) / 32, (unsigned)U), 256, 0, st, x,
-                            (const double*)part, X, p.parts, p.M, p.N, p.ldx, p.tall, eps))
+                            (const double*)part, X, p.parts, p.M, p.N, p.ldx, p.tall, kHalf ? 1 : 2, eps))
         return rc;
-    auto product = [&](const CUtensorMap& first, const CUtensorMap& second, int tiles, int K, PParams q) {
+    auto product = [&](auto config, const orth::Maps& maps, int tiles, int K, PParams q) {
+        using C = decltype(config);
         q.kblocks = (K + orth::KB - 1) / orth::KB;
         q.M = p.M;
         q.N = p.N;
@@ -980,13 +995,15 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         q.cb = b;
         q.cc = c;
         q.scale = scale;
-        // few tiles: split K over a cluster, so that the SMs are filled and every CTA has two blocks
-        int S = 1;
-        while (S < orth::MAX_SPLIT && (long long)tiles * U * S * 2 <= dev->sms && q.kblocks >= 4 * S) S *= 2;
+        // few tiles: split K over a cluster.  One CTA per SM fits 72 clusters of 2, 33 of 4 or 15 of 8 on
+        // 148 SMs; every CTA keeps two K blocks
+        const long long clusters = tiles * U;
+        int S = clusters <= 15 * C::MINB ? 8 : clusters <= 33 * C::MINB ? 4 : clusters <= 72 * C::MINB ? 2 : 1;
+        while (S > 1 && q.kblocks < 2 * S) S /= 2;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)S, (unsigned)tiles, (unsigned)U);
         cfg.blockDim = dim3(orth::THREADS, 1, 1);
-        cfg.dynamicSmemBytes = orth::p_smem_bytes();
+        cfg.dynamicSmemBytes = C::SMEM;
         cfg.stream = st;
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -997,25 +1014,26 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, orth::product_kernel, first, second, q) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, orth::product_kernel<C>, maps, q) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
     };
     for (int k = 0; k < steps; ++k) {
         const bool odd = k & 1, last = k + 1 == steps;
-        const CUtensorMap &yk = odd ? zk : xk, &yn = odd ? zn : xn;
         PParams q = {};
         q.kind = orth::GRAM;
+        q.parts = 2;
         q.y = A;
+        q.y2 = Q;
         q.ld = p.lda;
-        if (int rc = product(yk, yk, tm * (tm + 1) / 2, p.N, q)) return rc;
+        if (int rc = product(GramC(), gram[odd], tm * (tm + 1) / 2, p.N, q)) return rc;
         q.kind = orth::POLY;
         q.y = P;
-        q.a = A;
-        if (int rc = product(ak, ak, tm * (tm + 1) / 2, p.M, q)) return rc;
-        q.kind = !last ? orth::NEXT : sizeof(T) == 2 ? orth::OUT_BF16 : orth::OUT_F32;
+        if (int rc = product(orth::Full(), poly, tm * (tm + 1) / 2, p.M, q)) return rc;
+        q.kind = !last ? orth::NEXT : kHalf ? orth::OUT_BF16 : orth::OUT_F32;
+        q.parts = kHalf ? 1 : 2;
         q.y = odd ? X : Z;
         q.ld = p.ldx;
         q.out = out;
-        if (int rc = product(pk, yn, tm * tn, p.M, q)) return rc;
+        if (int rc = product(NextC(), next[odd], tm * tn, p.M, q)) return rc;
     }
     return launched(2 + 3 * steps);
 }
