@@ -30,6 +30,7 @@
 #pragma once
 #include "common.cuh"
 #include <cuda_fp16.h>
+#include <type_traits>
 
 namespace orth {
 
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(256)
 constexpr int TM = 128, KB = 64;                     // tile of the output, K block
 constexpr int OPB = TM * KB * 2;                     // one operand's K block, 16 KB
 constexpr int MAX_SPLIT = 8;
-constexpr int THREADS = 64 + 128;                    // producer, issuer, four epilogue warps
+constexpr int THREADS = 64 + 256;                    // producer, issuer, eight epilogue warps
 constexpr float SQ = 512.f;                          // scale of stored Q
 
 enum Kind { GRAM = 0, POLY = 1, NEXT = 2, OUT_F32 = 3, OUT_BF16 = 4 };
@@ -114,7 +115,6 @@ enum Kind { GRAM = 0, POLY = 1, NEXT = 2, OUT_F32 = 3, OUT_BF16 = 4 };
 struct PParams {
     int kblocks;             // K blocks of the whole product
     int M, tiles_n;          // rows of X, A, Q and P; tiles along the columns (NEXT, OUT)
-    int kind;
     int ld;                  // row stride of the halves that are written (GRAM, POLY, NEXT), columns written
     int parts;               // 2: hi and lo are written, 1: hi alone
     __half* y;               // where they go, [u][hi, lo][M][ld]
@@ -128,9 +128,9 @@ struct PBars {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES], done;
     uint32_t tmem_base;
 };
-constexpr int STG = 72;  // padded row of the staged halves (64 columns); floats: 68
+constexpr int STG = 40;                             // padded row of 32 staged halves (16-byte rows); floats: 36
 constexpr int EXCHANGE = TM * TM * 4;               // the S partial slices of a tile
-constexpr int STAGED = TM / 2 * STG * 2 * 4;        // up to four arrays of half a tile's rows
+__host__ __device__ constexpr int stage_area(int rows) { return rows * STG * 2 * 4; }  // of one column half: four arrays of halves
 // What a product takes: FL, SL: the first / second operand's lo part as well; ACC accumulators for hi hi
 // (and one for the cross terms, if any); STAGES K blocks in flight; MINB CTAs on an SM.
 template <bool FL_, bool SL_, int ACC_, int STAGES_, int MINB_>
@@ -141,133 +141,103 @@ struct Config {
     static constexpr int ACCS = ACC + (FL || SL);
     static constexpr int COLS = ACCS == 1 ? 128 : ACCS == 2 ? 256 : 512;  // of tensor memory
     // the ring; over it the exchange and what is staged
-    static constexpr int RING = STAGES * STAGE > EXCHANGE + STAGED ? STAGES * STAGE : EXCHANGE + STAGED;
+    static constexpr int USED = EXCHANGE + 2 * stage_area(TM / 2);
+    static constexpr int RING = STAGES * STAGE > USED ? STAGES * STAGE : USED;
     static constexpr int SMEM = RING + (int)sizeof(PBars) + 1024;
+    static_assert(RING >= 2 * stage_area(TM), "");
     static_assert(MINB * COLS <= 512 && STAGES <= MAX_STAGES, "");
 };
 using Full = Config<true, true, 3, 3, 1>;      // hi hi + hi lo + lo hi, 192 KB ring
 using High = Config<false, false, 1, 3, 2>;    // hi hi, 96 KB
 using Left = Config<true, false, 1, 2, 2>;     // hi hi + lo hi, 96 KB
-__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 x = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-        const float2 f = __half22float2(x);
-        const __half2 r = __floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y);
-        h[i] = *reinterpret_cast<const uint32_t*>(&x);
-        l[i] = *reinterpret_cast<const uint32_t*>(&r);
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
+__device__ __forceinline__ void group_sync(int g) {
+    if (g == 0)
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+    else
+        asm volatile("bar.sync 2, 128;" ::: "memory");
 }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// four values as fp16 hi and lo
+__device__ __forceinline__ void split4(const float (&v)[4], uint2& hi, uint2& lo) {
+    const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+    const float2 fa = __half22float2(a), fb = __half22float2(b);
+    const __half2 c = __floats2half2_rn(v[0] - fa.x, v[1] - fa.y), d = __floats2half2_rn(v[2] - fb.x, v[3] - fb.y);
+    hi = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    lo = make_uint2(*reinterpret_cast<const uint32_t*>(&c), *reinterpret_cast<const uint32_t*>(&d));
+}
 
-// 16 adjacent values of the product at (row, col) of the matrix into the staging area: `sr` is the
-// row there, `sc` the column of the 64 that are staged.  Tall results go straight out: a warp's lanes
-// are adjacent rows, which are adjacent in memory.
-__device__ __forceinline__ void stage16(const PParams& p, int u, int row, int col, uint8_t* area, int rows, int sr, int sc,
-                                        float (&v)[16]) {
-    const float f = p.scale / (SX * SP);
-    if (p.kind >= OUT_F32) {
-        if (p.tall) {
-            if (row < p.M)
+// Four adjacent values of the product at (row, col) of the matrix into the staging area (`rows` rows, four
+// arrays y hi, y lo, y2 hi, y2 lo): `sr` is the row there, `sc` the column of the 32 that are staged.
+template <int KIND>
+__device__ __forceinline__ void stage4(const PParams& p, int row, int col, uint8_t* area, int rows, int sr, int sc, const float (&v)[4]) {
+    if constexpr (KIND == OUT_F32) {
+        const float f = p.scale / (SX * SP);
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(area) + sr * 36 + sc) = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+    } else if constexpr (KIND == OUT_BF16) {
+        const float f = p.scale / (SX * SP);
+        *reinterpret_cast<uint2*>(area + (sr * STG + sc) * 2) = make_uint2(pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f));
+    } else {
+        uint8_t* o = area + (sr * STG + sc) * 2;
+        const int arr = rows * STG * 2;
+        uint2 hi, lo;
+        float w[4];
+        constexpr float m = KIND == GRAM ? 1.f / SX : KIND == NEXT ? 1.f / SP : SP / (SX * SQ);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (col + e < p.N) {
-                        const long long at = ((long long)u * p.N + col + e) * p.M + row;
-                        if (p.kind == OUT_F32)
-                            static_cast<float*>(p.out)[at] = v[e] * f;
-                        else
-                            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v[e] * f);
-                    }
-        } else if (p.kind == OUT_F32) {
-            float* o = reinterpret_cast<float*>(area) + sr * 68 + sc;
+        for (int e = 0; e < 4; ++e) w[e] = v[e] * m + (KIND == POLY && row == col + e ? SP * p.ca : 0.f);
+        split4(w, hi, lo);
+        *reinterpret_cast<uint2*>(o) = hi;
+        *reinterpret_cast<uint2*>(o + arr) = lo;
+        if constexpr (KIND == GRAM) {  // Q = b I + c A, of the A that was computed, not of its rounded parts
+            const float f = SQ * p.cc / (SX * SX);
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(o + e) = make_float4(v[e] * f, v[e + 1] * f, v[e + 2] * f, v[e + 3] * f);
-        } else {
-            uint32_t* o = reinterpret_cast<uint32_t*>(area) + (sr * STG + sc) / 2;
-#pragma unroll
-            for (int e = 0; e < 8; e += 4)
-                *reinterpret_cast<uint4*>(o + e) =
-                    make_uint4(pack_bf16(v[2 * e] * f, v[2 * e + 1] * f), pack_bf16(v[2 * e + 2] * f, v[2 * e + 3] * f),
-                               pack_bf16(v[2 * e + 4] * f, v[2 * e + 5] * f), pack_bf16(v[2 * e + 6] * f, v[2 * e + 7] * f));
-        }
-        return;
-    }
-    __half* o = reinterpret_cast<__half*>(area) + sr * STG + sc;
-    const int arr = rows * STG;  // halves of one staged array: y hi, y lo, y2 hi, y2 lo
-    uint4 hi, lo;
-    float w[16];
-    const float m = p.kind == GRAM ? 1.f / SX : p.kind == NEXT ? 1.f / SP : SP / (SX * SQ);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = v[e] * m + (p.kind == POLY && row == col + e ? SP * p.ca : 0.f);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        split8(w + 8 * h, hi, lo);
-        *reinterpret_cast<uint4*>(o + 8 * h) = hi;
-        if (p.parts == 2) *reinterpret_cast<uint4*>(o + arr + 8 * h) = lo;
-    }
-    if (p.kind == GRAM) {
-        // Q = b I + c A of the A that was computed, not of its rounded parts
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = SQ * (p.cc / (SX * SX) * v[e] + (row == col + e ? p.cb : 0.f));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            split8(w + 8 * h, hi, lo);
-            *reinterpret_cast<uint4*>(o + 2 * arr + 8 * h) = hi;
-            *reinterpret_cast<uint4*>(o + 3 * arr + 8 * h) = lo;
+            for (int e = 0; e < 4; ++e) w[e] = v[e] * f + (row == col + e ? SQ * p.cb : 0.f);
+            split4(w, hi, lo);
+            *reinterpret_cast<uint2*>(o + 2 * arr) = hi;
+            *reinterpret_cast<uint2*>(o + 3 * arr) = lo;
         }
     }
 }
-// The staged 64 columns of `rows` rows (matrix rows row0.., columns col0..) out to memory, by 128 threads
-__device__ __forceinline__ void flush64(const PParams& p, int u, int row0, int col0, const uint8_t* area, int rows, int tid) {
-    const long long mat = (long long)p.M * p.ld;
-    if (p.kind >= OUT_F32) {
-        if (p.tall) return;
-        const long long base = (long long)u * p.M * p.N;
-        const int per = p.kind == OUT_F32 ? 4 : 8, lanes = 64 / per;  // 16-byte pieces of a row
+// The staged 32 columns of `rows` rows (matrix rows row0.., columns col0..) out to memory, by 128 threads
+template <int KIND>
+__device__ __forceinline__ void flush32(const PParams& p, int u, int row0, int col0, const uint8_t* area, int rows, int tid) {
+    if constexpr (KIND >= OUT_F32) {
+        using T = std::conditional_t<KIND == OUT_F32, float, __nv_bfloat16>;
+        constexpr int per = 16 / sizeof(T), lanes = 32 / per, pitch = KIND == OUT_F32 ? 36 : STG;
+        const T* s = reinterpret_cast<const T*>(area);
+        T* out = static_cast<T*>(p.out) + (long long)u * p.M * p.N;
+        if (p.tall) {  // out [N][M]: adjacent threads take adjacent rows of the tile
+#pragma unroll 1
+            for (int i = tid; i < rows * 32; i += 128) {
+                const int r = i % rows, c = i / rows;
+                if (row0 + r < p.M && col0 + c < p.N) out[(long long)(col0 + c) * p.M + row0 + r] = s[r * pitch + c];
+            }
+            return;
+        }
         const bool whole = p.N % per == 0;
+#pragma unroll 1
         for (int i = tid; i < rows * lanes; i += 128) {
             const int r = i / lanes, c = i % lanes * per;
-            if (row0 + r >= p.M) continue;
-            const long long at = base + (long long)(row0 + r) * p.N + col0 + c;
-            if (p.kind == OUT_F32) {
-                const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(area) + r * 68 + c);
-                float* o = static_cast<float*>(p.out) + at;
-                if (whole) {
-                    if (col0 + c < p.N) *reinterpret_cast<float4*>(o) = x;
-                } else {
-                    const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col0 + c + e < p.N) o[e] = xs[e];
-                }
+            if (row0 + r >= p.M || col0 + c >= p.N) continue;
+            T* o = out + (long long)(row0 + r) * p.N + col0 + c;
+            if (whole) {
+                *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(s + r * pitch + c);
             } else {
-                const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(area) + r * STG + c;
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-                if (whole) {
-                    if (col0 + c < p.N) *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(s);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (col0 + c + e < p.N) o[e] = s[e];
-                }
+#pragma unroll 1
+                for (int e = 0; e < per && col0 + c + e < p.N; ++e) o[e] = s[r * pitch + c + e];
             }
         }
-        return;
-    }
-    const int arrays = p.kind == GRAM ? 4 : p.parts;
-    for (int a = 0; a < arrays; ++a) {
-        __half* y = (a < 2 ? p.y : p.y2) + ((long long)u * 2 + (a & 1)) * mat;
-        if (a == 1 && p.parts == 1) continue;
-        const __half* s = reinterpret_cast<const __half*>(area) + a * rows * STG;
-        for (int i = tid; i < rows * 8; i += 128) {
-            const int r = i / 8, c = i % 8 * 8;
-            if (row0 + r < p.M && col0 + c < p.ld)
-                *reinterpret_cast<uint4*>(y + (long long)(row0 + r) * p.ld + col0 + c) =
-                    *reinterpret_cast<const uint4*>(s + r * STG + c);
+    } else {
+        const long long mat = (long long)p.M * p.ld;
+#pragma unroll 1
+        for (int a = 0; a < (KIND == GRAM ? 4 : p.parts); ++a) {
+            __half* y = (KIND != GRAM || a < 2 ? p.y : p.y2) + ((long long)u * 2 + (a & 1)) * mat;
+            const uint8_t* s = area + a * rows * STG * 2;
+#pragma unroll 2
+            for (int i = tid; i < rows * 4; i += 128) {
+                const int r = i / 4, c = i % 4 * 8;
+                if (row0 + r < p.M && col0 + c < p.ld)
+                    *reinterpret_cast<uint4*>(y + (long long)(row0 + r) * p.ld + col0 + c) =
+                        *reinterpret_cast<const uint4*>(s + (r * STG + c) * 2);
+            }
         }
     }
 }
@@ -289,7 +259,7 @@ __device__ __forceinline__ void load_symmetric(uint8_t* dst, const CUtensorMap* 
 struct Maps {
     CUtensorMap first_k, first_mn, second_k, second_mn;
 };
-template <typename C>
+template <typename C, int KIND>
 __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_constant__ Maps maps, const PParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_align<1024>(smem_raw);
@@ -297,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
     const int S = gridDim.x, r = blockIdx.x, u = blockIdx.z;  // cluster (S, 1, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int bi, bj;
-    if (p.kind <= POLY) {  // tile of the upper triangle, column by column
+    if (KIND <= POLY) {  // tile of the upper triangle, column by column
         bj = 0;
         int t = blockIdx.y;
         while (t > bj) t -= ++bj;
@@ -309,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
     const int per = (p.kblocks + S - 1) / S, k0 = min(r * per, p.kblocks), nk = min(per, p.kblocks - k0);
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&maps.first_k);
-        tma_prefetch_desc(p.kind <= POLY ? &maps.second_k : &maps.second_mn);
+        tma_prefetch_desc(KIND <= POLY ? &maps.second_k : &maps.second_mn);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 1);
@@ -335,15 +305,15 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
                 const int k = (k0 + i) * KB;
                 mbar_expect_tx(bar, C::STAGE);
                 for (int part = 0; part < 1 + C::FL; ++part, dst += OPB) {
-                    if (p.kind == GRAM)
+                    if (KIND == GRAM)
                         tma_load_3d(dst, &maps.first_k, k, bi * TM, 2 * u + part, bar);
                     else
                         load_symmetric(dst, &maps.first_k, &maps.first_mn, bi, k, 2 * u + part, bar);
                 }
                 for (int part = 0; part < 1 + C::SL; ++part, dst += OPB) {
-                    if (p.kind == GRAM) {
+                    if (KIND == GRAM) {
                         tma_load_3d(dst, &maps.second_k, k, bj * TM, 2 * u + part, bar);
-                    } else if (p.kind == POLY) {
+                    } else if (KIND == POLY) {
                         load_symmetric(dst, &maps.second_k, &maps.second_mn, bj, k, 2 * u + part, bar);
                     } else {
                         tma_load_3d(dst, &maps.second_mn, bj * TM, k, 2 * u + part, bar);
@@ -359,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
                 const int slot = i % C::STAGES, t = (k0 + i) * KB / TM;
                 mbar_wait(&bars->full[slot], (i / C::STAGES) & 1, TTT_DEVERR_TIMEOUT_TMA);
                 tc::fence_after();
-                const int fm = p.kind != GRAM && t < bi, sm = p.kind >= NEXT || (p.kind == POLY && t < bj);  // MN-major
+                const int fm = KIND != GRAM && t < bi, sm = KIND >= NEXT || (KIND == POLY && t < bj);  // MN-major
                 const uint32_t fb = smem_u32(ring + slot * C::STAGE), sb = fb + (1 + C::FL) * OPB;
                 const uint64_t fh = tc::smem_desc(fb, fm ? OPB / 2 : 16, 1024, 2), sh = tc::smem_desc(sb, sm ? OPB / 2 : 16, 1024, 2);
                 const uint64_t lo = OPB >> 4, fstep = fm ? 128 : 2, sstep = sm ? 128 : 2;
@@ -379,22 +349,19 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
             tc::commit(&bars->done);
         }
     }
-    const int tid = threadIdx.x - 64, q4 = warp & 3;
-    const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
+    // Epilogue: two groups of four warps, group g taking columns 64 g .. 64 g + 63; a warp reads the 32
+    // lanes (rows) of its quarter of tensor memory.
+    const int g = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int used = nk > 0 ? (nk - 1) * C::ACC / nk + 1 : 0;
     // columns c .. c + 15 of the accumulators' sum, in the thread's row
     auto take = [&](int c, float (&v)[16]) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = 0.f;
-        if (nk == 0) return;
-        float x[16];
-        if (C::FL || C::SL) {
-            tc::ld16(lane_base + C::ACC * TM + c, x);
-            tc::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = x[e];
-        }
-        for (int a = 0; a < used; ++a) {
+#pragma unroll 1
+        for (int a = C::FL || C::SL ? C::ACC : used - 1; a >= 0; a = a > used ? used - 1 : a - 1) {
+            if (nk == 0) break;
+            float x[16];
             tc::ld16(lane_base + a * TM + c, x);
             tc::wait_ld();
 #pragma unroll
@@ -407,16 +374,20 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
             tc::fence_after();
         }
         if (S == 1) {
-            const int row = q4 * 32 + lane;
-            for (int h = 0; h < 2; ++h) {
-                for (int c = 0; c < 64; c += 16) {
+            uint8_t* area = ring + g * stage_area(TM);
+#pragma unroll 1
+            for (int c0 = 64 * g; c0 < 64 * g + 64; c0 += 32) {
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
                     float v[16];
-                    take(64 * h + c, v);
-                    stage16(p, u, bi * TM + row, bj * TM + 64 * h + c, ring, TM, row, c, v);
+                    take(c0 + c, v);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        stage4<KIND>(p, bi * TM + row, bj * TM + c0 + c + e, area, TM, row, c + e, {v[e], v[e + 1], v[e + 2], v[e + 3]});
                 }
-                epilogue_sync();
-                flush64(p, u, bi * TM, bj * TM + 64 * h, ring, TM, tid);
-                epilogue_sync();
+                group_sync(g);
+                flush32<KIND>(p, u, bi * TM, bj * TM + c0, area, TM, tid);
+                group_sync(g);
             }
         }
     }
@@ -425,33 +396,39 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
         float* buf = reinterpret_cast<float*>(ring);   // [S][128 columns][R], over the ring
         cluster_sync_all();  // every CTA's MMAs have read their operands: the rings are free
         if (warp >= 2) {
-            const int row = q4 * 32 + lane;
-            const uint32_t to = dsmem_map(buf + r * TM * R + row % R, row / R);
-            for (int c = 0; c < TM; c += 16) {
+            float* here = buf + r * TM * R + row % R;
+            const uint32_t there = dsmem_map(here, row / R);
+#pragma unroll 1
+            for (int c = 64 * g; c < 64 * g + 64; c += 16) {
                 float v[16];
                 take(c, v);
+                if (row / R == r)
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4u * R * (c + e)), "f"(v[e]) : "memory");
+                    for (int e = 0; e < 16; ++e) here[R * (c + e)] = v[e];
+                else
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + 4u * R * (c + e)), "f"(v[e]) : "memory");
             }
         }
         cluster_sync_all();
         if (warp >= 2) {
-            uint8_t* area = ring + TM * TM * 4;
-            const int groups = 128 / R, row = tid % R, g = tid / R;  // threads of a group: the slice's rows
-            for (int h = 0; h < 2; ++h) {
-                for (int c = 16 * g; c < 64; c += 16 * groups) {
-                    float v[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+            uint8_t* area = ring + EXCHANGE + g * stage_area(R);
+            const int pw = R / 4, sr = tid % R, sc = tid / R * pw;  // a thread's columns of each 32
+#pragma unroll 1
+            for (int c0 = 64 * g; c0 < 64 * g + 64; c0 += 32) {
+#pragma unroll 1
+                for (int c = sc; c < sc + pw; c += 4) {
+                    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
                     for (int s = 0; s < S; ++s)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] += buf[(s * TM + 64 * h + c + e) * R + row];
-                    stage16(p, u, bi * TM + r * R + row, bj * TM + 64 * h + c, area, R, row, c, v);
+                        for (int e = 0; e < 4; ++e) v[e] += buf[(s * TM + c0 + c + e) * R + sr];
+                    stage4<KIND>(p, bi * TM + r * R + sr, bj * TM + c0 + c, area, R, sr, c, v);
                 }
-                epilogue_sync();
-                flush64(p, u, bi * TM + r * R, bj * TM + 64 * h, area, R, tid);
-                epilogue_sync();
+                group_sync(g);
+                flush32<KIND>(p, u, bi * TM + r * R, bj * TM + c0, area, R, tid);
+                group_sync(g);
             }
         }
     }

@@ -929,6 +929,9 @@ int orth_check(int steps, float a, float b, float c, float eps) {
         return TTT_ERR_INVALID_ARG;
     return orth_coef_ok(a, b, c, steps) ? TTT_OK : TTT_ERR_UNSUPPORTED;
 }
+template <int K>
+using Kind = std::integral_constant<int, K>;
+
 // out = scale * (Newton-Schulz steps of x); T: the type of x and out
 template <typename T>
 int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, float b, float c, float eps,
@@ -974,18 +977,16 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
     constexpr bool kHalf = sizeof(T) == 2;  // bf16: X is held in one fp16 number
     using GramC = std::conditional_t<kHalf, orth::High, orth::Full>;
     using NextC = std::conditional_t<kHalf, orth::Left, orth::Full>;
-    static SmemRecord gram_smem, poly_smem, next_smem;
-    if (!allow_smem(orth::product_kernel<GramC>, GramC::SMEM, gram_smem) ||
-        !allow_smem(orth::product_kernel<orth::Full>, orth::Full::SMEM, poly_smem) ||
-        !allow_smem(orth::product_kernel<NextC>, NextC::SMEM, next_smem))
-        return TTT_ERR_CUDA;
     if (int rc = launch_pdl(orth::square_kernel<T>, dim3((unsigned)p.parts, (unsigned)U), orth::TPB, 0, st, x, part, mn))
         return rc;
     if (int rc = launch_pdl(orth::start_kernel<T>, dim3((p.ldx + 31) / 32, (p.M + 31) / 32, (unsigned)U), 256, 0, st, x,
                             (const double*)part, X, p.parts, p.M, p.N, p.ldx, p.tall, kHalf ? 1 : 2, eps))
         return rc;
-    auto product = [&](auto config, const orth::Maps& maps, int tiles, int K, PParams q) {
+    auto product = [&](auto config, auto kind, const orth::Maps& maps, int tiles, int K, PParams q) {
         using C = decltype(config);
+        const auto kern = orth::product_kernel<C, kind()>;
+        static SmemRecord record;
+        if (!allow_smem(kern, C::SMEM, record)) return (int)TTT_ERR_CUDA;
         q.kblocks = (K + orth::KB - 1) / orth::KB;
         q.M = p.M;
         q.N = p.N;
@@ -999,6 +1000,8 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         // 148 SMs; every CTA keeps two K blocks
         const long long clusters = tiles * U;
         int S = clusters <= 15 * C::MINB ? 8 : clusters <= 33 * C::MINB ? 4 : clusters <= 72 * C::MINB ? 2 : 1;
+        if (C::ACC > 1)  // full precision: no more than 16 K blocks in an accumulator chain
+            while (S < 8 && q.kblocks > 16 * S) S *= 2;
         while (S > 1 && q.kblocks < 2 * S) S /= 2;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)S, (unsigned)tiles, (unsigned)U);
@@ -1014,26 +1017,25 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, orth::product_kernel<C>, maps, q) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, kern, maps, q) == cudaSuccess ? (int)TTT_OK : (int)TTT_ERR_CUDA;
     };
     for (int k = 0; k < steps; ++k) {
         const bool odd = k & 1, last = k + 1 == steps;
         PParams q = {};
-        q.kind = orth::GRAM;
         q.parts = 2;
         q.y = A;
         q.y2 = Q;
         q.ld = p.lda;
-        if (int rc = product(GramC(), gram[odd], tm * (tm + 1) / 2, p.N, q)) return rc;
-        q.kind = orth::POLY;
+        if (int rc = product(GramC(), Kind<orth::GRAM>(), gram[odd], tm * (tm + 1) / 2, p.N, q)) return rc;
         q.y = P;
-        if (int rc = product(orth::Full(), poly, tm * (tm + 1) / 2, p.M, q)) return rc;
-        q.kind = !last ? orth::NEXT : kHalf ? orth::OUT_BF16 : orth::OUT_F32;
+        if (int rc = product(orth::Full(), Kind<orth::POLY>(), poly, tm * (tm + 1) / 2, p.M, q)) return rc;
         q.parts = kHalf ? 1 : 2;
         q.y = odd ? X : Z;
         q.ld = p.ldx;
         q.out = out;
-        if (int rc = product(NextC(), next[odd], tm * tn, p.M, q)) return rc;
+        const int rc = last ? product(NextC(), Kind<kHalf ? orth::OUT_BF16 : orth::OUT_F32>(), next[odd], tm * tn, p.M, q)
+                            : product(NextC(), Kind<orth::NEXT>(), next[odd], tm * tn, p.M, q);
+        if (rc) return rc;
     }
     return launched(2 + 3 * steps);
 }
