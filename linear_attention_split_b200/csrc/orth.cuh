@@ -196,49 +196,79 @@ __device__ __forceinline__ void stage4(const PParams& p, int row, int col, uint8
         }
     }
 }
-// The staged 32 columns of `rows` rows (matrix rows row0.., columns col0..) out to memory, by 128 threads
-template <int KIND>
-__device__ __forceinline__ void flush32(const PParams& p, int u, int row0, int col0, const uint8_t* area, int rows, int tid) {
+// The staged 32 columns of ROWS rows (matrix rows row0.., columns col0..) out to memory, by 128 threads
+template <int KIND, int ROWS>
+__device__ __forceinline__ void flush32(const PParams& p, int u, int row0, int col0, const uint8_t* area, int tid) {
     if constexpr (KIND >= OUT_F32) {
         using T = std::conditional_t<KIND == OUT_F32, float, __nv_bfloat16>;
         constexpr int per = 16 / sizeof(T), lanes = 32 / per, pitch = KIND == OUT_F32 ? 36 : STG;
         const T* s = reinterpret_cast<const T*>(area);
         T* out = static_cast<T*>(p.out) + (long long)u * p.M * p.N;
         if (p.tall) {  // out [N][M]: adjacent threads take adjacent rows of the tile
-#pragma unroll 1
-            for (int i = tid; i < rows * 32; i += 128) {
-                const int r = i % rows, c = i / rows;
-                if (row0 + r < p.M && col0 + c < p.N) out[(long long)(col0 + c) * p.M + row0 + r] = s[r * pitch + c];
-            }
+            const int r = tid % ROWS;
+            T* o = out + (long long)(col0 + tid / ROWS) * p.M + row0 + r;
+            if (row0 + r < p.M)
+#pragma unroll 8
+                for (int c = tid / ROWS; c < 32; c += 128 / ROWS, o += (long long)(128 / ROWS) * p.M)
+                    if (col0 + c < p.N) *o = s[r * pitch + c];
             return;
         }
         const bool whole = p.N % per == 0;
-#pragma unroll 1
-        for (int i = tid; i < rows * lanes; i += 128) {
-            const int r = i / lanes, c = i % lanes * per;
-            if (row0 + r >= p.M || col0 + c >= p.N) continue;
-            T* o = out + (long long)(row0 + r) * p.N + col0 + c;
-            if (whole) {
-                *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(s + r * pitch + c);
-            } else {
-#pragma unroll 1
-                for (int e = 0; e < per && col0 + c + e < p.N; ++e) o[e] = s[r * pitch + c + e];
+        const int c = tid % lanes * per;
+        constexpr int STEP = 128 / lanes;
+        T* o = out + (long long)(row0 + tid / lanes) * p.N + col0 + c;
+        if (col0 + c < p.N)
+#pragma unroll
+            for (int r = tid / lanes; r < ROWS; r += STEP, o += (long long)STEP * p.N) {
+                if (row0 + r >= p.M) break;
+                if (whole) {
+                    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(s + r * pitch + c);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < per; ++e)
+                        if (col0 + c + e < p.N) o[e] = s[r * pitch + c + e];
+                }
             }
-        }
     } else {
         const long long mat = (long long)p.M * p.ld;
-#pragma unroll 1
-        for (int a = 0; a < (KIND == GRAM ? 4 : p.parts); ++a) {
-            __half* y = (KIND != GRAM || a < 2 ? p.y : p.y2) + ((long long)u * 2 + (a & 1)) * mat;
-            const uint8_t* s = area + a * rows * STG * 2;
-#pragma unroll 2
-            for (int i = tid; i < rows * 4; i += 128) {
-                const int r = i / 4, c = i % 4 * 8;
-                if (row0 + r < p.M && col0 + c < p.ld)
-                    *reinterpret_cast<uint4*>(y + (long long)(row0 + r) * p.ld + col0 + c) =
-                        *reinterpret_cast<const uint4*>(s + (r * STG + c) * 2);
-            }
+        const int c = tid % 4 * 8, r0 = tid / 4;  // 32 rows at a time
+        if (col0 + c >= p.ld) return;
+        const long long at = u * 2 * mat + (long long)(row0 + r0) * p.ld + col0 + c;
+#pragma unroll
+        for (int a = 0; a < (KIND == GRAM ? 4 : 2); ++a) {
+            if (a == 1 && KIND == NEXT && p.parts == 1) break;
+            __half* y = (a < 2 ? p.y : p.y2) + at + (a & 1) * mat;
+            const uint8_t* s = area + (a * ROWS * STG + r0 * STG + c) * 2;
+#pragma unroll
+            for (int r = 0; r < (ROWS + 31) / 32; ++r)
+                if (32 * r + r0 < ROWS && row0 + 32 * r + r0 < p.M)
+                    *reinterpret_cast<uint4*>(y + (long long)(32 * r) * p.ld) = *reinterpret_cast<const uint4*>(s + 32 * r * STG * 2);
         }
+    }
+}
+// The slice of 128 / S rows that this CTA owns, columns col0 .. col0 + 63: the S partials added in rank order
+template <int KIND, int S>
+__device__ __forceinline__ void finish_slice(const PParams& p, int u, int row0, int col0, const float* buf, uint8_t* areas, int g,
+                                             int tid) {
+    constexpr int R = TM / S, PW = R / 4;  // rows; a thread's columns of each 32
+    uint8_t* area = areas + g * stage_area(R);
+    const int sr = tid % R, sc = tid / R * PW;
+#pragma unroll 1
+    for (int c0 = 0; c0 < 64; c0 += 32) {
+        const float* b = buf + (64 * g + c0 + sc) * R + sr;
+        float v[PW];
+#pragma unroll
+        for (int c = 0; c < PW; ++c) v[c] = b[c * R];
+#pragma unroll
+        for (int s = 1; s < S; ++s)
+#pragma unroll
+            for (int c = 0; c < PW; ++c) v[c] += b[(s * TM + c) * R];
+#pragma unroll
+        for (int c = 0; c < PW; c += 4)
+            stage4<KIND>(p, row0 + sr, col0 + c0 + sc + c, area, R, sr, sc + c, {v[c], v[c + 1], v[c + 2], v[c + 3]});
+        group_sync(g);
+        flush32<KIND, R>(p, u, row0, col0 + c0, area, tid);
+        group_sync(g);
     }
 }
 
@@ -356,17 +386,17 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
     const int used = nk > 0 ? (nk - 1) * C::ACC / nk + 1 : 0;
     // columns c .. c + 15 of the accumulators' sum, in the thread's row
     auto take = [&](int c, float (&v)[16]) {
+        float x[C::ACCS][16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-#pragma unroll 1
-        for (int a = C::FL || C::SL ? C::ACC : used - 1; a >= 0; a = a > used ? used - 1 : a - 1) {
-            if (nk == 0) break;
-            float x[16];
-            tc::ld16(lane_base + a * TM + c, x);
-            tc::wait_ld();
+        for (int a = 0; a < C::ACCS; ++a) tc::ld16(lane_base + a * TM + c, x[a]);
+        tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] += x[e];
-        }
+        for (int e = 0; e < 16; ++e) v[e] = C::FL || C::SL ? (used > 0 ? x[C::ACC][e] : 0.f) : 0.f;
+#pragma unroll
+        for (int a = 0; a < C::ACC; ++a)
+            if (a < used)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] += x[a][e];
     };
     if (warp >= 2) {
         if (nk > 0) {
@@ -377,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
             uint8_t* area = ring + g * stage_area(TM);
 #pragma unroll 1
             for (int c0 = 64 * g; c0 < 64 * g + 64; c0 += 32) {
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < 32; c += 16) {
                     float v[16];
                     take(c0 + c, v);
@@ -386,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
                         stage4<KIND>(p, bi * TM + row, bj * TM + c0 + c + e, area, TM, row, c + e, {v[e], v[e + 1], v[e + 2], v[e + 3]});
                 }
                 group_sync(g);
-                flush32<KIND>(p, u, bi * TM, bj * TM + c0, area, TM, tid);
+                flush32<KIND, TM>(p, u, bi * TM, bj * TM + c0, area, tid);
                 group_sync(g);
             }
         }
@@ -413,23 +443,13 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
         }
         cluster_sync_all();
         if (warp >= 2) {
-            uint8_t* area = ring + EXCHANGE + g * stage_area(R);
-            const int pw = R / 4, sr = tid % R, sc = tid / R * pw;  // a thread's columns of each 32
-#pragma unroll 1
-            for (int c0 = 64 * g; c0 < 64 * g + 64; c0 += 32) {
-#pragma unroll 1
-                for (int c = sc; c < sc + pw; c += 4) {
-                    float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-                    for (int s = 0; s < S; ++s)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] += buf[(s * TM + c0 + c + e) * R + sr];
-                    stage4<KIND>(p, bi * TM + r * R + sr, bj * TM + c0 + c, area, R, sr, c, v);
-                }
-                group_sync(g);
-                flush32<KIND>(p, u, bi * TM + r * R, bj * TM + c0, area, R, tid);
-                group_sync(g);
-            }
+            const int row0 = bi * TM + r * R, col0 = bj * TM + 64 * g;
+            if (S == 2)
+                finish_slice<KIND, 2>(p, u, row0, col0, buf, ring + EXCHANGE, g, tid);
+            else if (S == 4)
+                finish_slice<KIND, 4>(p, u, row0, col0, buf, ring + EXCHANGE, g, tid);
+            else
+                finish_slice<KIND, 8>(p, u, row0, col0, buf, ring + EXCHANGE, g, tid);
         }
     }
     tc::fence_before();

@@ -929,6 +929,28 @@ int orth_check(int steps, float a, float b, float c, float eps) {
         return TTT_ERR_INVALID_ARG;
     return orth_coef_ok(a, b, c, steps) ? TTT_OK : TTT_ERR_UNSUPPORTED;
 }
+// The split of K over a cluster that is fastest by count: a K block's MMAs take 67 cycles per 128 x 128 x
+// 16 (four per product), a tile's start and end about 4500 and the exchange about 3500, and 148 SMs hold
+// 148, 72, 33 or 15 clusters of 1, 2, 4 or 8.  (384 x 1536: X X^T, 24 blocks and 6 tiles, 8 ways; P X, 6
+// blocks and 36 tiles, not at all.)  Full precision takes no more than 16 K blocks in an accumulator chain
+// where it can.
+template <typename C>
+int orth_split(long long tiles, int kblocks) {
+    const int room[4] = {148, 72, 33, 15};
+    const long long block = 4 * 67 * (1 + C::FL + C::SL);
+    int best = 1;
+    long long least = 0;
+    for (int i = 0, S = 1; i < 4; ++i, S *= 2) {
+        if (S > 1 && kblocks < 2 * S) break;
+        const long long per = (kblocks + S - 1) / S, waves = (tiles + room[i] * C::MINB - 1) / (room[i] * C::MINB);
+        const long long cycles = waves * (per * block * C::MINB + 4500 + (S > 1 ? 3500 : 0));
+        if (i == 0 || cycles < least || (C::ACC > 1 && (kblocks + best - 1) / best > 16)) {
+            best = S;
+            least = cycles;
+        }
+    }
+    return best;
+}
 template <int K>
 using Kind = std::integral_constant<int, K>;
 
@@ -996,13 +1018,7 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         q.cb = b;
         q.cc = c;
         q.scale = scale;
-        // few tiles: split K over a cluster.  One CTA per SM fits 72 clusters of 2, 33 of 4 or 15 of 8 on
-        // 148 SMs; every CTA keeps two K blocks
-        const long long clusters = tiles * U;
-        int S = clusters <= 15 * C::MINB ? 8 : clusters <= 33 * C::MINB ? 4 : clusters <= 72 * C::MINB ? 2 : 1;
-        if (C::ACC > 1)  // full precision: no more than 16 K blocks in an accumulator chain
-            while (S < 8 && q.kblocks > 16 * S) S *= 2;
-        while (S > 1 && q.kblocks < 2 * S) S /= 2;
+        const int S = orth_split<C>((long long)tiles * U, q.kblocks);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)S, (unsigned)tiles, (unsigned)U);
         cfg.blockDim = dim3(orth::THREADS, 1, 1);
