@@ -11,7 +11,12 @@
 // Angles of far positions need more than 32 bits: the position times the frequency in turns
 // (theta / 2 pi) is formed and reduced to [-1/2, 1/2] in fp64, then sincospi in fp32 of that
 // fraction (error about 1e-7).  A block does this once per (token, pair) of its token tile and
-// keeps the table in shared memory for all its heads and both tensors.
+// keeps the table in shared memory for its heads and both tensors.
+//
+// The bound is HBM (one read and one write of Q and K).  A thread takes VEC adjacent pairs: two
+// loads of VEC features (16 bytes each where dims, strides and pointers are multiples of 16 bytes;
+// the largest power of two that divides them all otherwise), two table reads, two stores.  A unit
+// (its place in the head) is fixed for a thread; it walks rows, several loads in flight.
 #pragma once
 #include "common.cuh"
 
@@ -35,6 +40,8 @@ struct Params {
     const float* pos;      // [N][axes] or [B][N][axes], or null: the grid in raster order
     long long pos_b;       // stride of a batch entry, 0 when shared
     int B, H, N, d, TN;
+    int heads;             // heads of a block
+    int units, tail;       // units of a head: pairs / VEC turned, then tail / VEC passed on
     int interleaved;
     float sign;            // -1: inverse
     Axes ax;
@@ -42,14 +49,32 @@ struct Params {
     double turns[MAX_D / 2];  // frequency of each pair / 2 pi
 };
 
-template <typename T>
-__global__ void __launch_bounds__(THREADS)
+// VEC features as they lie in memory
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Lane {
+    T v[VEC];
+};
+
+// The rotation, written so that every variant rounds alike (the compiler chooses no contraction)
+__device__ __forceinline__ void turn(float x, float y, float c, float s, float& a, float& b) {
+    a = fmaf(x, c, -__fmul_rn(y, s));
+    b = fmaf(y, c, __fmul_rn(x, s));
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(THREADS, 4)
     rope_kernel(const T* q, const T* k, T* qout, T* kout, const __grid_constant__ Params p) {
-    extern __shared__ float2 table[];  // [TN][pairs]: cos, sin
+    extern __shared__ __align__(16) float table[];  // [TN][pairs] cos, then the same of sin
+    using L = Lane<T, VEC>;
+    constexpr int FLY = sizeof(L) == 16 ? 2 : 4;  // rows of a thread that are in flight
     const int t0 = blockIdx.x * p.TN, tn = min(p.TN, p.N - t0);
     const int b = blockIdx.z, P = p.ax.pairs;
+    float *cosines = table, *sines = table + p.TN * P;
+    // launched with programmatic stream serialization: the table of a token grid depends on nothing the
+    // previous grid wrote, so it overlaps that grid's tail
+    if (p.pos) griddep_wait();
     for (int i = threadIdx.x; i < tn * P; i += THREADS) {
-        const int t = i / P, j = i % P, tok = t0 + t;
+        const int t = i / P, j = i - t * P, tok = t0 + t;
         int a = 0;
         while (a + 1 < p.ax.n && 2 * j >= p.ax.at[a + 1]) ++a;
         double x;
@@ -64,37 +89,92 @@ __global__ void __launch_bounds__(THREADS)
         r -= rint(r);
         float sn, cs;
         sincospif(2.f * (float)r, &sn, &cs);
-        table[t * P + j] = make_float2(cs, p.sign * sn);
+        cosines[i] = cs;
+        sines[i] = p.sign * sn;
     }
+    if (!p.pos) griddep_wait();
+    griddep_launch();
     __syncthreads();
-    const int tail = p.d - 2 * P, items = P + tail;
-    const int heads = (p.H + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * heads, hn = min(heads, p.H - h0);
-    const int both = k ? 2 : 1;
-    for (int i = threadIdx.x; i < both * hn * tn * items; i += THREADS) {
-        const int it = i % items;
-        int rest = i / items;
-        const int t = rest % tn;
-        rest /= tn;
-        const int h = h0 + rest % hn;
-        const bool is_k = rest / hn > 0;
-        const View vi = is_k ? p.ki : p.qi, vo = is_k ? p.ko : p.qo;
-        const T* src = (is_k ? k : q) + b * vi.b + h * vi.h + (t0 + t) * vi.n;
-        T* dst = (is_k ? kout : qout) + b * vo.b + h * vo.h + (t0 + t) * vo.n;
-        if (it >= P) {
-            dst[P + it] = src[P + it];
-            continue;
-        }
-        int e1 = 2 * it, e2 = 2 * it + 1;
-        if (!p.interleaved) {
+    // threads are laid out [rows at a time][units]; a row is (tensor, head, token)
+    const int all = p.units + p.tail, rpp = max(1, THREADS / all);
+    const int unit0 = threadIdx.x % all, r0 = threadIdx.x / all;
+    if (r0 >= rpp && all <= THREADS) return;
+    const int h0 = blockIdx.y * p.heads, hn = min(p.heads, p.H - h0);
+    const int rows = (k ? 2 : 1) * hn * tn;
+    for (int unit = unit0; unit < all; unit += THREADS) {  // more than one pass only for heads wider than the block
+        int e1 = 2 * VEC * unit, e2 = e1 + VEC, j = VEC * unit;
+        const bool turned = unit < p.units;
+        if (!turned) {
+            e1 = e2 = 2 * P + (unit - p.units) * VEC;
+        } else if (!p.interleaved) {
             int a = 0;
-            while (a + 1 < p.ax.n && 2 * it >= p.ax.at[a + 1]) ++a;
-            e1 = p.ax.at[a] / 2 + it;
+            while (a + 1 < p.ax.n && 2 * j >= p.ax.at[a + 1]) ++a;
+            e1 = p.ax.at[a] / 2 + j;
             e2 = e1 + p.ax.dims[a] / 2;
         }
-        const float2 cs = table[t * P + it];
-        const float x = to_f(src[e1]), y = to_f(src[e2]);
-        dst[e1] = from_f<T>(x * cs.x - y * cs.y);
-        dst[e2] = from_f<T>(y * cs.x + x * cs.y);
+        for (int first = r0; first < rows; first += FLY * rpp) {
+            L x[FLY], y[FLY];
+            T* dst[FLY];
+            int tok[FLY];
+#pragma unroll
+            for (int f = 0; f < FLY; ++f) {
+                const int row = first + f * rpp;
+                if (row >= rows) break;
+                const int hh = row / tn, t = row - hh * tn;
+                const bool is_k = hh >= hn;
+                const int h = h0 + (is_k ? hh - hn : hh);
+                const View& vi = is_k ? p.ki : p.qi;
+                const View& vo = is_k ? p.ko : p.qo;
+                const T* src = (is_k ? k : q) + b * vi.b + h * vi.h + (t0 + t) * vi.n;
+                dst[f] = (is_k ? kout : qout) + b * vo.b + h * vo.h + (t0 + t) * vo.n;
+                tok[f] = t;
+                x[f] = *reinterpret_cast<const L*>(src + e1);
+                if (turned) y[f] = *reinterpret_cast<const L*>(src + e2);
+            }
+#pragma unroll
+            for (int f = 0; f < FLY; ++f) {
+                if (first + f * rpp >= rows) break;
+                if (!turned) {
+                    *reinterpret_cast<L*>(dst[f] + e1) = x[f];
+                    continue;
+                }
+                const float *cp = cosines + tok[f] * P + j, *sp = sines + tok[f] * P + j;
+                float c[VEC], s[VEC];
+                if constexpr (VEC >= 4) {
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 4) {
+                        const float4 cv = *reinterpret_cast<const float4*>(cp + e), sv = *reinterpret_cast<const float4*>(sp + e);
+                        c[e] = cv.x, c[e + 1] = cv.y, c[e + 2] = cv.z, c[e + 3] = cv.w;
+                        s[e] = sv.x, s[e + 1] = sv.y, s[e + 2] = sv.z, s[e + 3] = sv.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) c[e] = cp[e], s[e] = sp[e];
+                }
+                L o1, o2;
+                if (p.interleaved) {  // pairs are neighbours: VEC pairs in the 2 VEC features of x, y
+                    float in[2 * VEC], out[2 * VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) in[e] = to_f(x[f].v[e]), in[VEC + e] = to_f(y[f].v[e]);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        turn(in[2 * e], in[2 * e + 1], c[e], s[e], out[2 * e], out[2 * e + 1]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o1.v[e] = from_f<T>(out[e]), o2.v[e] = from_f<T>(out[VEC + e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        float a, d;
+                        turn(to_f(x[f].v[e]), to_f(y[f].v[e]), c[e], s[e], a, d);
+                        o1.v[e] = from_f<T>(a);
+                        o2.v[e] = from_f<T>(d);
+                    }
+                }
+                *reinterpret_cast<L*>(dst[f] + e1) = o1;
+                *reinterpret_cast<L*>(dst[f] + e2) = o2;
+            }
+        }
     }
 }
 

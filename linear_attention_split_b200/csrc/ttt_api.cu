@@ -1728,22 +1728,53 @@ int ttt_rope(const void* q, const void* k, void* q_out, void* k_out, const float
     for (int t = 0; t < 4; ++t) *v[t] = {s[t][0], s[t][1], s[t][2]};
     DeviceInfo* dev = nullptr;
     if (int rc = current_device(&dev)) return rc;
-    p.TN = std::max(1, std::min(16, 4096 / p.ax.pairs));
-    const int tiles = (N + p.TN - 1) / p.TN;
+    // features of one load: the largest power of two (16 bytes at most) that divides sections, tail,
+    // strides and pointers
+    int vec = 16 / (int)es;
+    auto divides = [&](int v) {
+        if ((d - at) % v || (interleaved && at / 2 % v)) return false;
+        for (int a = 0; a < axes; ++a)
+            if (!interleaved && axis_dims[a] / 2 % v) return false;
+        const void* ptr[4] = {q, k, q_out, k_out};
+        for (int t = 0; t < 4; ++t) {
+            if (reinterpret_cast<uintptr_t>(ptr[t]) % (v * es)) return false;
+            if (!ptr[t]) continue;
+            if ((B > 1 && s[t][0] % v) || (H > 1 && s[t][1] % v) || (N > 1 && s[t][2] % v)) return false;
+        }
+        return true;
+    };
+    while (vec > 1 && !divides(vec)) vec /= 2;
+    p.units = at / 2 / vec;
+    p.tail = (d - at) / vec;
+    // 16 tokens to a block and all heads, unless that leaves SMs without a block
+    auto blocks = [&](int tn, int hg) { return (long long)((N + tn - 1) / tn) * B * hg; };
     int hg = 1;
-    while (hg < H && (long long)tiles * B * hg < 2LL * dev->sms) ++hg;
-    const dim3 g((unsigned)tiles, (unsigned)std::min(hg, 65535), (unsigned)B);
+    p.TN = 16;
+    while (hg < H && blocks(p.TN, hg) < 2LL * dev->sms) hg = std::min(H, 2 * hg);
+    while (p.TN > 4 && blocks(p.TN, hg) < dev->sms) p.TN /= 2;
+    p.heads = (H + hg - 1) / hg;
+    const dim3 g((unsigned)((N + p.TN - 1) / p.TN), (unsigned)((H + p.heads - 1) / p.heads), (unsigned)B);
     const int smem = p.TN * p.ax.pairs * 8;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto run = [&](auto t, auto v) {
+        using T = decltype(t);
+        return launch_pdl(rope::rope_kernel<T, v()>, g, rope::THREADS, smem, st, static_cast<const T*>(q), static_cast<const T*>(k),
+                          static_cast<T*>(q_out), static_cast<T*>(k_out), p);
+    };
+    using std::integral_constant;
+    int rc;
     if (dtype == TTT_BF16) {
         using T = __nv_bfloat16;
-        rope::rope_kernel<T><<<g, rope::THREADS, smem, st>>>(static_cast<const T*>(q), static_cast<const T*>(k),
-                                                             static_cast<T*>(q_out), static_cast<T*>(k_out), p);
+        rc = vec == 8   ? run(T(), integral_constant<int, 8>())
+             : vec == 4 ? run(T(), integral_constant<int, 4>())
+             : vec == 2 ? run(T(), integral_constant<int, 2>())
+                        : run(T(), integral_constant<int, 1>());
     } else {
-        using T = float;
-        rope::rope_kernel<T><<<g, rope::THREADS, smem, st>>>(static_cast<const T*>(q), static_cast<const T*>(k),
-                                                             static_cast<T*>(q_out), static_cast<T*>(k_out), p);
+        rc = vec == 4   ? run(0.f, integral_constant<int, 4>())
+             : vec == 2 ? run(0.f, integral_constant<int, 2>())
+                        : run(0.f, integral_constant<int, 1>());
     }
+    if (rc) return rc;
     return launched(1);
 }
 
