@@ -19,45 +19,34 @@ namespace lnorm {
 constexpr int THREADS = 256;    // threads of a block with rows of up to 8 warps; wider rows take one block each
 constexpr int MAX_EPT = 16;     // elements of a row that one thread holds at most
 constexpr int MAX_COLS = 1024 * MAX_EPT;
+constexpr int STRANDS = 32;     // of the sum over blocks
 
+// VEC adjacent elements as they lie in memory
 template <typename T, int VEC>
-struct Pack;
-template <>
-struct Pack<float, 1> {
-    static __device__ __forceinline__ void load(const float* p, float* v) { v[0] = *p; }
-    static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
-};
-template <>
-struct Pack<float, 4> {
-    static __device__ __forceinline__ void load(const float* p, float* v) {
-        const float4 x = *reinterpret_cast<const float4*>(p);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    }
-    static __device__ __forceinline__ void store(float* p, const float* v) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-};
-template <>
-struct Pack<__nv_bfloat16, 1> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* v) { v[0] = __bfloat162float(*p); }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) { *p = __float2bfloat16_rn(v[0]); }
-};
-template <>
-struct Pack<__nv_bfloat16, 8> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* v) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+struct alignas(sizeof(T) * VEC) Pack {
+    T v[VEC];
+    __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int e = 0; e < VEC; ++e) f[e] = to_f(v[e]);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                                  pack_bf16(v[6], v[7]));
+    __device__ __forceinline__ void set(const float* f) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = from_f<T>(f[e]);
     }
 };
+template <int VEC>
+__device__ __forceinline__ void get_weights(const float* w, float* f) {
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(w + e));
+            f[e] = x.x, f[e + 1] = x.y, f[e + 2] = x.z, f[e + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = __ldg(w + e);
+    }
+}
 
 // How a block is split over rows: `lanes` threads of a warp (a power of two) times `warps` warps
 // hold one row (warps > 1 only with lanes = 32).
@@ -66,124 +55,165 @@ struct Shape {
     __host__ __device__ int rows_per_block() const { return threads / (lanes * warps); }
 };
 
-// Sum of K values over the threads of one row.  Within a warp by exchange; across warps through
-// `red` ([2][K][32], `which` alternates so that one barrier per round is enough), in warp order.
+// Sums of K values over the threads of one row.  Within a warp by exchange; across warps through
+// `red` ([K][32]), in warp order.  Buffers of successive rounds have to differ.
 template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], const Shape s, float* red, int which) {
+__device__ __forceinline__ void row_sum(float (&v)[K], const Shape s, float* red) {
     for (int o = s.lanes >> 1; o > 0; o >>= 1)
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     if (s.warps == 1) return;
     const int warp = threadIdx.x >> 5, first = warp / s.warps * s.warps;
-    float* r = red + which * K * 32;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) r[k * 32 + warp] = v[k];
+        for (int k = 0; k < K; ++k) red[k * 32 + warp] = v[k];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         v[k] = 0.f;
-        for (int w = 0; w < s.warps; ++w) v[k] += r[k * 32 + first + w];
+        for (int w = 0; w < s.warps; ++w) v[k] += red[k * 32 + first + w];
     }
 }
 
 // ----------------------------------------------------------------------------- forward ---
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(1024)
+// A group of threads takes FLY rows at once: their loads are in flight together, and weight and bias
+// are read once for all of them.
+template <typename T, int VEC, int NV, int FLY, int MAXT>
+__global__ void __launch_bounds__(MAXT)
     forward_kernel(const T* x, const float* __restrict__ gamma, const float* __restrict__ beta, T* y, int rows, int C,
                    float eps, float inv_c, const Shape s) {
-    __shared__ float red[2 * 2 * 32];
+    using L = Pack<T, VEC>;
+    __shared__ float red[3 * FLY * 32];
     const int tpr = s.lanes * s.warps, rpb = s.rows_per_block();
     const int at = threadIdx.x % tpr;
-    const long long row = (long long)blockIdx.x * rpb + threadIdx.x / tpr;
-    const bool live = row < rows;
-    const long long base = row * C;
-    float v[NV][VEC];
-    float s1[1] = {0.f};
+    const long long row0 = (long long)blockIdx.x * rpb * FLY + threadIdx.x / tpr;
+    griddep_wait();
+    griddep_launch();
+    float v[FLY][NV][VEC];
+    float s1[FLY];
+    L raw[FLY][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (at + i * tpr) * VEC;
-        if (live && c < C)
-            Pack<T, VEC>::load(x + base + c, v[i]);
-        else
+    for (int f = 0; f < FLY; ++f)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
+        for (int i = 0; i < NV; ++i) {
+            const long long row = row0 + f * rpb;
+            const int c = (at + i * tpr) * VEC;
+            if (row < rows && c < C) raw[f][i] = *reinterpret_cast<const L*>(x + row * C + c);
+        }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s1[0] += v[i][e];
+    for (int f = 0; f < FLY; ++f) {
+        s1[f] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (row0 + f * rpb < rows && (at + i * tpr) * VEC < C)
+                raw[f][i].get(v[f][i]);
+            else
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[f][i][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s1[f] += v[f][i][e];
+        }
     }
-    row_sum<1>(s1, s, red, 0);
-    const float mean = s1[0] * inv_c;
-    float s2[2] = {0.f, 0.f};
+    row_sum<FLY>(s1, s, red);
+    float s2[2 * FLY];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool in = (at + i * tpr) * VEC < C;
+    for (int f = 0; f < FLY; ++f) {
+        const float mean = s1[f] * inv_c;
+        s2[2 * f] = s2[2 * f + 1] = 0.f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            v[i][e] -= mean;
-            if (in) {
-                s2[0] += v[i][e];
-                s2[1] = fmaf(v[i][e], v[i][e], s2[1]);
+        for (int i = 0; i < NV; ++i) {
+            const bool in = (at + i * tpr) * VEC < C;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                v[f][i][e] = in ? v[f][i][e] - mean : 0.f;
+                s2[2 * f] += v[f][i][e];
+                s2[2 * f + 1] = fmaf(v[f][i][e], v[f][i][e], s2[2 * f + 1]);
             }
         }
     }
-    row_sum<2>(s2, s, red + 64, 0);
-    const float off = s2[0] * inv_c;
-    const float rstd = rsqrtf(fmaxf(s2[1] * inv_c - off * off, 0.f) + eps);
-    if (!live) return;
+    row_sum<2 * FLY>(s2, s, red + FLY * 32);
+    float off[FLY], rstd[FLY];
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+        off[f] = s2[2 * f] * inv_c;
+        rstd[f] = rsqrtf(fmaxf(s2[2 * f + 1] * inv_c - off[f] * off[f], 0.f) + eps);
+        if (s2[2 * f + 1] != s2[2 * f + 1]) rstd[f] = s2[2 * f + 1];  // a NaN is not clamped away
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (at + i * tpr) * VEC;
         if (c >= C) continue;
-        float g[VEC], o[VEC];
-        if constexpr (VEC == 8) {
-            Pack<float, 4>::load(gamma + c, g);
-            Pack<float, 4>::load(gamma + c + 4, g + 4);
-        } else {
-            Pack<float, VEC>::load(gamma + c, g);
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = (v[i][e] - off) * rstd * g[e];
+        float g[VEC], b[VEC];
+        get_weights<VEC>(gamma + c, g);
         if (beta)
+            get_weights<VEC>(beta + c, b);
+        else
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] += __ldg(beta + c + e);
-        Pack<T, VEC>::store(y + base + c, o);
+            for (int e = 0; e < VEC; ++e) b[e] = 0.f;
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) {
+            if (row0 + f * rpb >= rows) continue;
+            float o[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) o[e] = fmaf((v[f][i][e] - off[f]) * rstd[f], g[e], b[e]);
+            L out;
+            out.set(o);
+            *reinterpret_cast<L*>(y + (row0 + f * rpb) * C + c) = out;
+        }
     }
 }
 
 // ----------------------------------------------------------------------------- backward --
-// Each group of threads walks rows `group, group + groups, ...` and keeps its columns' sums of
-// dy xh and dy in registers; the block adds its groups' sums in order and writes one partial row
-// of each per block, part[block][2][C].
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(1024)
+// Each group of threads walks rows `group, group + groups, ...`, the next row's loads in flight while
+// one is worked on, and keeps its columns' sums of dy xh and dy in registers; the block adds its
+// groups' sums in order and writes one partial row of each, part[block][2][C].
+template <typename T, int VEC, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == THREADS ? 2 : 1)
     backward_kernel(const T* dy, const T* x, const float* __restrict__ gamma, T* dx, float* __restrict__ part, int rows,
                     int C, float eps, float inv_c, const Shape s) {
+    using L = Pack<T, VEC>;
     extern __shared__ float sums[];  // [rows_per_block][2][C] when a block holds several rows
-    __shared__ float red[2 * 32 + 2 * 4 * 32];
+    __shared__ float red[2][5 * 32];
     const int tpr = s.lanes * s.warps, rpb = s.rows_per_block();
     const int at = threadIdx.x % tpr, grp = threadIdx.x / tpr;
+    griddep_wait();
+    griddep_launch();
+    L rx[NV], rt[NV];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (at + i * tpr) * VEC;
+            if (row < rows && c < C) {
+                rx[i] = *reinterpret_cast<const L*>(x + row * C + c);
+                rt[i] = *reinterpret_cast<const L*>(dy + row * C + c);
+            }
+        }
+    };
+    const long long stride = (long long)gridDim.x * rpb;
+    long long r0 = (long long)blockIdx.x * rpb;
+    fetch(r0 + grp);
     float g[NV][VEC], dg[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (at + i * tpr) * VEC;
+        if (c < C)
+            get_weights<VEC>(gamma + c, g[i]);
+        else
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            g[i][e] = c < C ? __ldg(gamma + c + e) : 0.f;
-            dg[i][e] = db[i][e] = 0.f;
-        }
+            for (int e = 0; e < VEC; ++e) g[i][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dg[i][e] = db[i][e] = 0.f;
     }
-    int turn = 0;
-    for (long long r0 = (long long)blockIdx.x * rpb; r0 < rows; r0 += (long long)gridDim.x * rpb, turn ^= 1) {
-        const long long row = r0 + grp, base = row * C;
+    for (int turn = 0; r0 < rows; r0 += stride, turn ^= 1) {
+        const long long row = r0 + grp;
         const bool live = row < rows;
         float v[NV][VEC], t[NV][VEC];
         float s1[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (at + i * tpr) * VEC;
-            if (live && c < C) {
-                Pack<T, VEC>::load(x + base + c, v[i]);
-                Pack<T, VEC>::load(dy + base + c, t[i]);
+            if (live && (at + i * tpr) * VEC < C) {
+                rx[i].get(v[i]);
+                rt[i].get(t[i]);
             } else {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) v[i][e] = t[i][e] = 0.f;
@@ -191,7 +221,8 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s1[0] += v[i][e];
         }
-        row_sum<1>(s1, s, red, turn);
+        fetch(row + stride);
+        row_sum<1>(s1, s, red[turn]);
         const float mean = s1[0] * inv_c;
         float s4[4] = {0.f, 0.f, 0.f, 0.f};  // c, c^2, t, t c
 #pragma unroll
@@ -207,9 +238,10 @@ __global__ void __launch_bounds__(1024)
                 s4[3] = fmaf(tg, v[i][e], s4[3]);
             }
         }
-        row_sum<4>(s4, s, red + 64, turn);
+        row_sum<4>(s4, s, red[turn] + 32);
         const float off = s4[0] * inv_c;
-        const float rstd = rsqrtf(fmaxf(s4[1] * inv_c - off * off, 0.f) + eps);
+        float rstd = rsqrtf(fmaxf(s4[1] * inv_c - off * off, 0.f) + eps);
+        if (s4[1] != s4[1]) rstd = s4[1];  // a NaN is not clamped away
         const float mt = s4[2] * inv_c;
         const float mtx = (s4[3] * inv_c - off * mt) * rstd;  // mean(t xh)
         if (live)
@@ -225,7 +257,9 @@ __global__ void __launch_bounds__(1024)
                     dg[i][e] = fmaf(t[i][e], xh, dg[i][e]);
                     db[i][e] += t[i][e];
                 }
-                Pack<T, VEC>::store(dx + base + c, o);
+                L out;
+                out.set(o);
+                *reinterpret_cast<L*>(dx + row * C + c) = out;
             }
     }
     float* p = part + (long long)blockIdx.x * 2 * C;
@@ -243,6 +277,7 @@ __global__ void __launch_bounds__(1024)
         __syncthreads();
         for (int c = threadIdx.x; c < 2 * C; c += blockDim.x) {
             float a = 0.f;
+#pragma unroll 8
             for (int r = 0; r < rpb; ++r) a += sums[r * 2 * C + c];
             p[c] = a;
         }
@@ -260,22 +295,25 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// dg, db = the partials' sums over the blocks, in block order within each of 8 strands, the
-// strands then in order.  32 columns x 8 strands per block.
-__global__ void __launch_bounds__(256)
+// dg, db = the partials' sums over the blocks: 32 columns x 32 strands per block, a strand adding every
+// 32nd partial in order (their loads in flight together), the strands then added in order.
+__global__ void __launch_bounds__(32 * STRANDS)
     finish_kernel(const float* __restrict__ part, float* __restrict__ dgamma, float* __restrict__ dbeta, int blocks,
                   int C) {
-    __shared__ float sm[8][33];
+    __shared__ float sm[STRANDS][33];
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), strand = threadIdx.x >> 5;
+    griddep_wait();
+    griddep_launch();
     float a = 0.f;
     if (col < 2 * C)
-        for (int b = strand; b < blocks; b += 8) a += part[(long long)b * 2 * C + col];
+#pragma unroll 10
+        for (int b = strand; b < blocks; b += STRANDS) a += part[(long long)b * 2 * C + col];
     sm[strand][threadIdx.x & 31] = a;
     __syncthreads();
     if (strand == 0 && col < 2 * C) {
         float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) t += sm[w][threadIdx.x & 31];
+        for (int w = 0; w < STRANDS; ++w) t += sm[w][threadIdx.x];
         if (col < C)
             dgamma[col] = t;
         else if (dbeta)

@@ -799,7 +799,8 @@ NormPlan norm_plan(int C, int dtype) {
     p.vec = C % full == 0 ? full : 1;
     const int vecs = C / p.vec, most = lnorm::MAX_EPT / p.vec;
     p.nv = most;
-    while (p.nv > 1 && p.nv * 16 > vecs) p.nv /= 2;  // short rows: a lane per vector first
+    while (p.nv > 1 && p.nv * 16 > vecs) p.nv = p.nv == 12 ? 8 : p.nv / 2;  // short rows: a lane per vector first
+    if (p.nv == 16 && (vecs + 31) / 32 <= 12) p.nv = 12;
     const int need = (vecs + p.nv - 1) / p.nv;
     if (need <= 32) {
         p.s.lanes = 1;
@@ -813,35 +814,32 @@ NormPlan norm_plan(int C, int dtype) {
     p.s.threads = tpr >= lnorm::THREADS ? tpr : lnorm::THREADS / tpr * tpr;
     return p;
 }
+// f(type, elements of a load, loads of a thread, threads of a block at most)
 template <typename F>
 int norm_dispatch(const NormPlan& p, int dtype, F f) {
-    using bf = __nv_bfloat16;
     using std::integral_constant;
-    if (dtype == TTT_BF16) {
-        if (p.vec == 8) return p.nv == 1 ? f(bf(), integral_constant<int, 8>(), integral_constant<int, 1>())
-                                         : f(bf(), integral_constant<int, 8>(), integral_constant<int, 2>());
-        switch (p.nv) {
-            case 1: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 1>());
-            case 2: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 2>());
-            case 4: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 4>());
-            case 8: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 8>());
-            default: return f(bf(), integral_constant<int, 1>(), integral_constant<int, 16>());
+    auto by_threads = [&](auto t, auto vec, auto nv) {
+        return p.s.threads <= lnorm::THREADS ? f(t, vec, nv, integral_constant<int, lnorm::THREADS>())
+               : p.s.threads <= 512          ? f(t, vec, nv, integral_constant<int, 512>())
+                                             : f(t, vec, nv, integral_constant<int, 1024>());
+    };
+    auto by_nv = [&](auto t, auto vec) -> int {
+        constexpr int V = decltype(vec)::value;
+        if (p.nv == 1) return by_threads(t, vec, integral_constant<int, 1>());
+        if constexpr (V <= 8)
+            if (p.nv == 2) return by_threads(t, vec, integral_constant<int, 2>());
+        if constexpr (V <= 4)
+            if (p.nv == 4) return by_threads(t, vec, integral_constant<int, 4>());
+        if constexpr (V == 1) {
+            if (p.nv == 8) return by_threads(t, vec, integral_constant<int, 8>());
+            if (p.nv == 12) return by_threads(t, vec, integral_constant<int, 12>());
+            return by_threads(t, vec, integral_constant<int, 16>());
         }
-    }
-    if (p.vec == 4) {
-        switch (p.nv) {
-            case 1: return f(float(), integral_constant<int, 4>(), integral_constant<int, 1>());
-            case 2: return f(float(), integral_constant<int, 4>(), integral_constant<int, 2>());
-            default: return f(float(), integral_constant<int, 4>(), integral_constant<int, 4>());
-        }
-    }
-    switch (p.nv) {
-        case 1: return f(float(), integral_constant<int, 1>(), integral_constant<int, 1>());
-        case 2: return f(float(), integral_constant<int, 1>(), integral_constant<int, 2>());
-        case 4: return f(float(), integral_constant<int, 1>(), integral_constant<int, 4>());
-        case 8: return f(float(), integral_constant<int, 1>(), integral_constant<int, 8>());
-        default: return f(float(), integral_constant<int, 1>(), integral_constant<int, 16>());
-    }
+        return TTT_ERR_UNSUPPORTED;
+    };
+    if (dtype == TTT_BF16)
+        return p.vec == 8 ? by_nv(__nv_bfloat16(), integral_constant<int, 8>()) : by_nv(__nv_bfloat16(), integral_constant<int, 1>());
+    return p.vec == 4 ? by_nv(float(), integral_constant<int, 4>()) : by_nv(float(), integral_constant<int, 1>());
 }
 // blocks of the backward pass: two per SM, fewer for few rows
 int norm_bwd_blocks(const NormPlan& p, int rows) {
@@ -1633,11 +1631,24 @@ int ttt_layernorm(const void* x, const float* gamma, const float* beta, void* y,
     if (beta && !aligned16(beta)) return TTT_ERR_INVALID_ARG;
     const NormPlan p = norm_plan(C, dtype);
     const int rpb = p.s.rows_per_block();
-    return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv) {
+    DeviceInfo* dev = nullptr;
+    if (int rc = current_device(&dev)) return rc;
+    return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv, auto maxt) {
         using T = decltype(t);
-        lnorm::forward_kernel<T, vec(), nv()><<<(rows + rpb - 1) / rpb, p.s.threads, 0, static_cast<cudaStream_t>(stream)>>>(
-            static_cast<const T*>(x), gamma, beta, static_cast<T*>(y), rows, C, eps, (float)(1.0 / C), p.s);
-        return launched(1);
+        // rows of a thread in flight: up to 32 elements of it (4 rows at most), one while that leaves SMs
+        // without two blocks
+        constexpr int V = decltype(vec)::value * decltype(nv)::value;
+        constexpr int FLY = maxt() > lnorm::THREADS ? 1 : V <= 8 ? 4 : V <= 16 ? 2 : 1;
+        auto run = [&](auto fly) {
+            const long long per = (long long)rpb * fly();
+            if (int rc = launch_pdl(lnorm::forward_kernel<T, vec(), nv(), fly(), maxt()>, dim3((unsigned)((rows + per - 1) / per)),
+                                    p.s.threads, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(x), gamma, beta,
+                                    static_cast<T*>(y), rows, C, eps, (float)(1.0 / C), p.s))
+                return rc;
+            return launched(1);
+        };
+        if (FLY > 1 && rows >= 2LL * dev->sms * rpb * FLY) return run(std::integral_constant<int, FLY>());
+        return run(std::integral_constant<int, 1>());
     });
 }
 
@@ -1659,12 +1670,15 @@ int ttt_layernorm_bwd(const void* dy, const void* x, const float* gamma, void* d
     const int smem = rpb > 1 ? rpb * 2 * C * 4 : 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     float* part = static_cast<float*>(workspace);
-    return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv) {
+    return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv, auto maxt) {
         using T = decltype(t);
-        lnorm::backward_kernel<T, vec(), nv()><<<blocks, p.s.threads, smem, st>>>(
-            static_cast<const T*>(dy), static_cast<const T*>(x), gamma, static_cast<T*>(dx), part, rows, C, eps,
-            (float)(1.0 / C), p.s);
-        lnorm::finish_kernel<<<(2 * C + 31) / 32, 256, 0, st>>>(part, dgamma, dbeta, blocks, C);
+        if (int rc = launch_pdl(lnorm::backward_kernel<T, vec(), nv(), maxt()>, dim3((unsigned)blocks), p.s.threads, smem, st,
+                                static_cast<const T*>(dy), static_cast<const T*>(x), gamma, static_cast<T*>(dx), part, rows, C, eps,
+                                (float)(1.0 / C), p.s))
+            return rc;
+        if (int rc = launch_pdl(lnorm::finish_kernel, dim3((2 * C + 31) / 32), 32 * lnorm::STRANDS, 0, st, (const float*)part, dgamma,
+                                dbeta, blocks, C))
+            return rc;
         return launched(2);
     });
 }

@@ -397,7 +397,7 @@ def _call(fn, dev, stream, *args):
         st = torch._C._cuda_getCurrentRawStream(dev)
     else:
         st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -417,16 +417,31 @@ def _rows(x):
 
 
 def _vector(t, C, name):
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (C,) or not t.is_contiguous()):
+    if t is not None and (t.dtype is not torch.float32 or t.dim() != 1 or t.shape[0] != C or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous fp32 tensor [C]")
+
+
+def _dense(first, *more):
+    """The library's type of dense tensors of one dtype and shape."""
+    dtype, shape = first.dtype, first.shape
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if not first.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    for t in more:
+        if t.dtype is not dtype:
+            raise TypeError("tensors must share one dtype")
+        if t.shape != shape:
+            raise ValueError("tensors must have one shape")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors")
+    return _DT[dtype]
 
 
 def ttt_layernorm(x, gamma, beta, y, eps=1e-6, stream=None):
     """Layer norm over the last axis: x, y [..., C] (y may be x); gamma, beta [C] fp32, beta may be None."""
-    dt = _dtype(x, y)
+    dt = _dense(x, y)
     rows, C = _rows(x)
-    if y.shape != x.shape:
-        raise ValueError("x and y must have one shape")
     _vector(gamma, C, "gamma")
     _vector(beta, C, "beta")
     dev = _one_device(x, gamma, beta, y)
@@ -440,10 +455,8 @@ def ttt_layernorm_bwd_workspace_bytes(rows, C, dtype):
 
 def ttt_layernorm_bwd(dy, x, gamma, dx, dgamma, dbeta=None, eps=1e-6, workspace=None, stream=None):
     """Gradients of ttt_layernorm: dx [..., C] (may be dy or x), dgamma and dbeta [C] fp32 (dbeta may be None)."""
-    dt = _dtype(dy, x, dx)
+    dt = _dense(x, dy, dx)
     rows, C = _rows(x)
-    if dy.shape != x.shape or dx.shape != x.shape:
-        raise ValueError("dy, x and dx must have one shape")
     for t, name in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")):
         _vector(t, C, name)
     dev = _one_device(x, dy, gamma, dx, dgamma, dbeta)
@@ -514,9 +527,9 @@ def ttt_orthogonalize_workspace_bytes(U, m, n, dtype):
 
 def ttt_orthogonalize(x, out, steps=5, coef=NS_COEF, eps=1e-7, scale=1.0, workspace=None, stream=None):
     """out = scale * the Newton-Schulz steps of each matrix of x [..., m, n] (out may be x)."""
-    dt = _dtype(x, out)
-    if x.dim() < 2 or out.shape != x.shape:
-        raise ValueError("x and out must have one shape [..., m, n]")
+    dt = _dense(x, out)
+    if x.dim() < 2:
+        raise ValueError("x must be [..., m, n]")
     dev = _one_device(x, out)
     m, n = x.shape[-2:]
     U = x.numel() // (m * n) if m * n else 0
@@ -534,10 +547,10 @@ def ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dtype):
 def ttt_linear_fullbatch_orth(q, k, v, w0, out, w_star=None, eta=0.1, steps=5, coef=NS_COEF, eps=1e-7, workspace=None,
                               stream=None):
     """TTT-Linear whose inner step goes along the orthogonalised gradient; tensors as for ttt_linear_fullbatch."""
-    dt = _dtype(q, k, v, out)
+    dt = _dense(q, k, v, out)
     _weights(w0, w_star)
-    if q.dim() != 4 or not q.shape == k.shape == v.shape == out.shape:
-        raise ValueError("q, k, v and out must have one shape [B, H, N, d]")
+    if q.dim() != 4:
+        raise ValueError("q, k, v and out must be [B, H, N, d]")
     B, H, N, d = q.shape
     if tuple(w0.shape) != (H, d, d) or (w_star is not None and tuple(w_star.shape) != (B, H, d, d)):
         raise ValueError("w0 must be [H, d, d] and w_star [B, H, d, d]")
