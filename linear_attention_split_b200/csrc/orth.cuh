@@ -9,14 +9,15 @@
 //
 // The products run on the fp16 tensor cores.  An operand is held as hi + lo, two fp16 numbers (about
 // 22 bits), and a product is hi hi + hi lo + lo hi accumulated in fp32.  fp32 matrices take all three
-// (result good to about 1e-6 of its norm).  For bf16 ones X is held as hi alone and only A Q, the
-// cheap product, and P hi + lo are taken in full: the iteration enlarges what is lost early by up to
-// a^5, and at s = 1 the polynomial cancels 3.4 - 4.8 + 2.0; in simulation bf16 operands leave 3e-2 of
-// the norm wrong, hi hi throughout 2e-3 to 3e-3, this choice 4e-4 to 8e-4, below the 1.7e-3 that
-// rounding the result to bf16 costs.  Values are bounded (|s| <= 2 throughout, checked on the host), so
-// fixed powers of two keep them inside fp16: X and A are stored times 2^12, P times 2^10, Q times 2^9.
+// (result good to about 2e-6 of its norm).  For bf16 ones X and P are held as hi alone and only the
+// product A Q is taken in full: the iteration enlarges what is lost early by up to a^5, and at s = 1 the
+// polynomial cancels 3.4 - 4.8 + 2.0, so A has to be exact where it meets itself.  In simulation bf16
+// operands leave 3e-2 of the result's norm wrong, hi hi throughout 2e-3 to 3e-3, this choice 0.9e-3 to
+// 1.4e-3, less than the 1.7e-3 that rounding the result to bf16 costs.  Values are bounded (|s| <= 2
+// throughout, checked on the host), so fixed powers of two keep them inside fp16: X and A are stored
+// times 2^12, P times 2^10, Q times 2^9.
 //
-// product_kernel: one 128 x 128 tile of a product per cluster; the K range is split over the S
+// product_kernel: one tile of 128 x 64, 128 or 256 of a product per cluster; the K range is split over the S
 // CTAs of the cluster when there are few tiles, and the partial tiles are exchanged through
 // distributed shared memory (each CTA adds one slice of rows, in rank order: deterministic).  Per CTA
 // a TMA producer and a tcgen05 issuer over a ring of 64-wide K blocks, and four epilogue warps, which
@@ -25,8 +26,8 @@
 // above the diagonal are formed, and an operand block below it is read from its mirror image as an
 // MN-major operand.  The tensor cores cut what falls below the accumulator's last bit at every
 // addition, about 1e-7 of the result for each: a full product therefore spreads its K blocks over
-// three accumulators and keeps the cross terms in a fourth, added in fp32 in the epilogue (1024 x 4096,
-// one accumulator: 2.4e-5 of the norm).
+// three or seven accumulators and keeps the cross terms in another, added in fp32 in the epilogue
+// (1024 x 4096, one accumulator: 2.4e-5 of the norm).
 #pragma once
 #include "common.cuh"
 #include <cuda_fp16.h>
@@ -35,20 +36,32 @@
 namespace orth {
 
 constexpr int TPB = 256;
-constexpr int MAX_PARTS = 64;
+constexpr int MAX_PARTS = 512;
 constexpr float SX = 4096.f, SP = 1024.f;  // scale of stored X and A, and of stored P
 
-// part[u][p] = sum of squares of piece p of matrix u
+// part[u][p] = sum of squares of piece p of matrix u; 16 bytes a load where the matrices allow it
 template <typename T>
 __global__ void __launch_bounds__(TPB) square_kernel(const T* __restrict__ x, double* __restrict__ part, long long mn) {
     __shared__ double sm[TPB / 32];
+    constexpr int VEC = 16 / sizeof(T);
+    struct alignas(16) Lane {
+        T v[VEC];
+    };
     griddep_wait();
     griddep_launch();
     const T* xu = x + blockIdx.y * mn;
+    const long long first = (long long)blockIdx.x * TPB + threadIdx.x, stride = (long long)gridDim.x * TPB;
     double s = 0.0;
-    for (long long i = (long long)blockIdx.x * TPB + threadIdx.x; i < mn; i += (long long)gridDim.x * TPB) {
-        const double v = (double)to_f(xu[i]);
-        s = fma(v, v, s);
+    if (mn % VEC == 0) {
+#pragma unroll 4
+        for (long long i = first; i < mn / VEC; i += stride) {
+            const Lane l = reinterpret_cast<const Lane*>(xu)[i];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s = fma((double)to_f(l.v[e]), (double)to_f(l.v[e]), s);
+        }
+    } else {
+#pragma unroll 4
+        for (long long i = first; i < mn; i += stride) s = fma((double)to_f(xu[i]), (double)to_f(xu[i]), s);
     }
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = s;
@@ -69,8 +82,16 @@ __device__ __forceinline__ double inverse_norm(double squares, float eps) {
     return isfinite(n) ? 1.0 / fmax(n, (double)eps) : (double)NAN;
 }
 
-// X [u][hi, lo][M][ld] (hi alone with halves = 1) from x (transposed on the way when tall), zero in columns N .. ld - 1.
-// 32 x 32 tiles through shared memory, so that both sides are read and written along rows.
+// the parts' sum, the same in every thread of the block (a warp's lanes take every 32nd, in order)
+__device__ __forceinline__ double sum_parts(const double* part, int parts) {
+    double s = 0.0;
+    for (int p = threadIdx.x & 31; p < parts; p += 32) s += part[p];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// X [u][hi, lo][M][ld] (hi alone with halves = 1) from x, zero in columns N .. ld - 1.  Any shape, a tall x
+// transposed on the way: 32 x 32 tiles through shared memory, so that both sides go along rows.
 template <typename T>
 __global__ void __launch_bounds__(256)
     start_kernel(const T* __restrict__ x, const double* __restrict__ part, __half* __restrict__ y, int parts, int M,
@@ -80,32 +101,61 @@ __global__ void __launch_bounds__(256)
     griddep_launch();
     const int u = blockIdx.z, i0 = blockIdx.y * 32, j0 = blockIdx.x * 32;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    double s = 0.0;
-    for (int p = 0; p < parts; ++p) s += part[(long long)u * parts + p];
-    const double inv = inverse_norm(s, eps);
     const T* xu = x + (long long)u * M * N;
-    for (int r = ty; r < 32; r += 8) {
-        const int i = tall ? i0 + tx : i0 + r, j = tall ? j0 + r : j0 + tx;
-        float v = 0.f;
-        if (i < M && j < N) v = (float)((double)to_f(xu[tall ? (long long)j * M + i : (long long)i * N + j]) * inv * SX);
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = ty + 8 * k, i = tall ? i0 + tx : i0 + r, j = tall ? j0 + r : j0 + tx;
+        v[k] = i < M && j < N ? to_f(xu[tall ? (long long)j * M + i : (long long)i * N + j]) : 0.f;
+    }
+    const double inv = inverse_norm(sum_parts(part + (long long)u * parts, parts), eps) * SX;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = ty + 8 * k;
+        const float f = (float)((double)v[k] * inv);
         if (tall)
-            sm[tx][r] = v;
+            sm[tx][r] = f;
         else
-            sm[r][tx] = v;
+            sm[r][tx] = f;
     }
     __syncthreads();
-    for (int r = ty; r < 32; r += 8) {
-        const int i = i0 + r, j = j0 + tx;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = i0 + ty + 8 * k, j = j0 + tx;
         if (i >= M || j >= ld) continue;
         __half* yu = y + (long long)u * 2 * M * ld + (long long)i * ld + j;
         __half lo;
-        split(sm[r][tx], yu[0], lo);
+        split(sm[ty + 8 * k][tx], yu[0], lo);
         if (halves == 2) yu[(long long)M * ld] = lo;
     }
 }
+// The same for wide matrices whose size is a multiple of 8 (then ld = N and nothing is padded): eight
+// adjacent values a thread.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    start8_kernel(const T* __restrict__ x, const double* __restrict__ part, __half* __restrict__ y, int parts, long long mn,
+                  int halves, float eps) {
+    struct alignas(16) Lane {
+        T v[8];
+    };
+    griddep_wait();
+    griddep_launch();
+    const long long u = blockIdx.y, i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8;
+    Lane l;
+    if (i < mn) l = *reinterpret_cast<const Lane*>(x + u * mn + i);
+    const double inv = inverse_norm(sum_parts(part + u * parts, parts), eps) * SX;
+    if (i >= mn) return;
+    __align__(16) __half hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split((float)((double)to_f(l.v[e]) * inv), hi[e], lo[e]);
+    __half* o = y + u * 2 * mn + i;
+    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(hi);
+    if (halves == 2) *reinterpret_cast<uint4*>(o + mn) = *reinterpret_cast<const uint4*>(lo);
+}
 
-constexpr int TM = 128, KB = 64;                     // tile of the output, K block
-constexpr int OPB = TM * KB * 2;                     // one operand's K block, 16 KB
+constexpr int TM = 128, KB = 64;                     // rows of a tile of the output, K block
+constexpr int PANEL = 64 * KB * 2;                   // a K block of 64 rows or columns, 8 KB
+constexpr int OPB = 2 * PANEL;                       // the first operand's K block
 constexpr int MAX_SPLIT = 8;
 constexpr int THREADS = 64 + 256;                    // producer, issuer, eight epilogue warps
 constexpr float SQ = 512.f;                          // scale of stored Q
@@ -123,33 +173,40 @@ struct PParams {
     int N, tall;
     float ca, cb, cc, scale;
 };
-constexpr int MAX_STAGES = 4;
+constexpr int MAX_STAGES = 8;
 struct PBars {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES], done;
     uint32_t tmem_base;
 };
 constexpr int STG = 40;                             // padded row of 32 staged halves (16-byte rows); floats: 36
-constexpr int EXCHANGE = TM * TM * 4;               // the S partial slices of a tile
 __host__ __device__ constexpr int stage_area(int rows) { return rows * STG * 2 * 4; }  // of one column half: four arrays of halves
-// What a product takes: FL, SL: the first / second operand's lo part as well; ACC accumulators for hi hi
-// (and one for the cross terms, if any); STAGES K blocks in flight; MINB CTAs on an SM.
-template <bool FL_, bool SL_, int ACC_, int STAGES_, int MINB_>
+// What a product takes: FL, SL: the first / second operand's lo part as well; BN columns of a tile; ACC
+// accumulators for hi hi (and one for the cross terms, if any); STAGES K blocks in flight.  One CTA on an SM.
+template <bool FL_, bool SL_, int BN_, int ACC_, int STAGES_>
 struct Config {
     static constexpr bool FL = FL_, SL = SL_;
-    static constexpr int ACC = ACC_, STAGES = STAGES_, MINB = MINB_;
-    static constexpr int STAGE = (2 + FL + SL) * OPB;
+    static constexpr int BN = BN_, ACC = ACC_, STAGES = STAGES_;
+    static constexpr int SECOND = BN / 64 * PANEL;                 // the second operand's K block
+    static constexpr int STAGE = (1 + FL) * OPB + (1 + SL) * SECOND;
     static constexpr int ACCS = ACC + (FL || SL);
-    static constexpr int COLS = ACCS == 1 ? 128 : ACCS == 2 ? 256 : 512;  // of tensor memory
+    static constexpr int COLS = ACCS * BN;                         // of tensor memory
+    static constexpr int EXCHANGE = BN > 128 ? 0 : TM * BN * 4;    // the S partial slices of a tile
     // the ring; over it the exchange and what is staged
     static constexpr int USED = EXCHANGE + 2 * stage_area(TM / 2);
     static constexpr int RING = STAGES * STAGE > USED ? STAGES * STAGE : USED;
     static constexpr int SMEM = RING + (int)sizeof(PBars) + 1024;
-    static_assert(RING >= 2 * stage_area(TM), "");
-    static_assert(MINB * COLS <= 512 && STAGES <= MAX_STAGES, "");
+    static_assert(RING >= 2 * stage_area(TM) && STAGES <= MAX_STAGES && COLS <= 512 && (COLS & (COLS - 1)) == 0, "");
+    // cycles of a K block: its MMAs (measured 53, 67 and 131 for 128 x 64, 128 and 256 x 16), or its loads at
+    // the 92 bytes a cycle that an SM gets
+    static constexpr int MMA = 4 * (1 + FL + SL) * (BN == 64 ? 53 : BN == 128 ? 67 : 131);
+    static constexpr int BLOCK = MMA > STAGE / 92 ? MMA : STAGE / 92;
 };
-using Full = Config<true, true, 3, 3, 1>;      // hi hi + hi lo + lo hi, 192 KB ring
-using High = Config<false, false, 1, 3, 2>;    // hi hi, 96 KB
-using Left = Config<true, false, 1, 2, 2>;     // hi hi + lo hi, 96 KB
+// hi hi + hi lo + lo hi, and hi hi alone
+template <int BN>
+using Full = Config<true, true, BN, BN == 64 ? 7 : 3, BN == 64 ? 4 : 3>;
+template <int BN>
+using High = Config<false, false, BN, 1, BN == 64 ? 8 : BN == 128 ? 6 : 4>;
+
 __device__ __forceinline__ void group_sync(int g) {
     if (g == 0)
         asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -236,7 +293,7 @@ __device__ __forceinline__ void flush32(const PParams& p, int u, int row0, int c
         const long long at = u * 2 * mat + (long long)(row0 + r0) * p.ld + col0 + c;
 #pragma unroll
         for (int a = 0; a < (KIND == GRAM ? 4 : 2); ++a) {
-            if (a == 1 && KIND == NEXT && p.parts == 1) break;
+            if (a == 1 && KIND != GRAM && p.parts == 1) break;
             __half* y = (a < 2 ? p.y : p.y2) + at + (a & 1) * mat;
             const uint8_t* s = area + (a * ROWS * STG + r0 * STG + c) * 2;
 #pragma unroll
@@ -246,23 +303,23 @@ __device__ __forceinline__ void flush32(const PParams& p, int u, int row0, int c
         }
     }
 }
-// The slice of 128 / S rows that this CTA owns, columns col0 .. col0 + 63: the S partials added in rank order
-template <int KIND, int S>
+// The slice of 128 / S rows that this CTA owns, columns col0 .. col0 + BN / 2 - 1: the S partials added in rank order
+template <int KIND, int BN, int S>
 __device__ __forceinline__ void finish_slice(const PParams& p, int u, int row0, int col0, const float* buf, uint8_t* areas, int g,
                                              int tid) {
     constexpr int R = TM / S, PW = R / 4;  // rows; a thread's columns of each 32
     uint8_t* area = areas + g * stage_area(R);
     const int sr = tid % R, sc = tid / R * PW;
 #pragma unroll 1
-    for (int c0 = 0; c0 < 64; c0 += 32) {
-        const float* b = buf + (64 * g + c0 + sc) * R + sr;
+    for (int c0 = 0; c0 < BN / 2; c0 += 32) {
+        const float* b = buf + (BN / 2 * g + c0 + sc) * R + sr;
         float v[PW];
 #pragma unroll
         for (int c = 0; c < PW; ++c) v[c] = b[c * R];
 #pragma unroll
         for (int s = 1; s < S; ++s)
 #pragma unroll
-            for (int c = 0; c < PW; ++c) v[c] += b[(s * TM + c) * R];
+            for (int c = 0; c < PW; ++c) v[c] += b[(s * BN + c) * R];
 #pragma unroll
         for (int c = 0; c < PW; c += 4)
             stage4<KIND>(p, row0 + sr, col0 + c0 + sc + c, area, R, sr, sc + c, {v[c], v[c + 1], v[c + 2], v[c + 3]});
@@ -272,41 +329,39 @@ __device__ __forceinline__ void finish_slice(const PParams& p, int u, int row0, 
     }
 }
 
-// One K block of a symmetric operand's rows t * 128 ..: K-major from its own tiles, which lie on or
-// above the diagonal, or from the mirror image, MN-major
-__device__ __forceinline__ void load_symmetric(uint8_t* dst, const CUtensorMap* km, const CUtensorMap* mn, int t, int k, int z,
-                                               uint64_t* bar) {
-    if (k / TM >= t) {
-        tma_load_3d(dst, km, k, t * TM, z, bar);
+// One K block of rows at .. at + rows - 1 of a symmetric operand: K-major from its own tiles, which lie on
+// or above the diagonal (in blocks of 128), or from the mirror image, MN-major in panels of 64
+__device__ __forceinline__ void load_symmetric(uint8_t* dst, const CUtensorMap* km, const CUtensorMap* mn, int at, int rows, int k,
+                                               int z, uint64_t* bar) {
+    if (k / TM >= at / TM) {
+        tma_load_3d(dst, km, k, at, z, bar);
     } else {
-        tma_load_3d(dst, mn, t * TM, k, z, bar);
-        tma_load_3d(dst + OPB / 2, mn, t * TM + 64, k, z, bar);
+        for (int c = 0; c < rows; c += 64) tma_load_3d(dst + c / 64 * PANEL, mn, at + c, k, z, bar);
     }
 }
 
-// Operands' tensor maps over [2 u + part][rows][ld], by rows of K (box 64 x 128: k) and by 64 x 64 blocks
-// (mn).  GRAM: both operands X, K-major.  POLY: A and Q, symmetric.  NEXT, OUT: P, symmetric, and X, MN-major.
+// Operands' tensor maps over [2 u + part][rows][ld], by rows of K (box 64 x 128, the second's 64 x BN: k)
+// and by 64 x 64 blocks (mn).  GRAM: both operands X, K-major.  POLY: A and Q, symmetric.  NEXT, OUT: P, symmetric, and X, MN-major.
 struct Maps {
     CUtensorMap first_k, first_mn, second_k, second_mn;
 };
 template <typename C, int KIND>
-__global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_constant__ Maps maps, const PParams p) {
+__global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ Maps maps, const PParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_align<1024>(smem_raw);
     PBars* bars = reinterpret_cast<PBars*>(ring + C::RING);
     const int S = gridDim.x, r = blockIdx.x, u = blockIdx.z;  // cluster (S, 1, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int bi, bj;
-    if (KIND <= POLY) {  // tile of the upper triangle, column by column
-        bj = 0;
+    int bi = blockIdx.y / p.tiles_n, bj = blockIdx.y % p.tiles_n;
+    if (KIND <= POLY) {  // tiles on or above the diagonal, row by row
         int t = blockIdx.y;
-        while (t > bj) t -= ++bj;
-        bi = t;
-    } else {
-        bi = blockIdx.y / p.tiles_n;
-        bj = blockIdx.y % p.tiles_n;
+        for (bi = 0; t >= p.tiles_n - bi * TM / C::BN; ++bi) t -= p.tiles_n - bi * TM / C::BN;
+        bj = bi * TM / C::BN + t;
     }
+    const int i0 = bi * TM, j0 = bj * C::BN;  // the tile's place
     const int per = (p.kblocks + S - 1) / S, k0 = min(r * per, p.kblocks), nk = min(per, p.kblocks - k0);
+    // accumulators for hi hi: `used` of them, each for a run of `len` of the 4 nk MMAs
+    const int len = (4 * nk + C::ACC - 1) / C::ACC, used = nk > 0 ? (4 * nk + len - 1) / len : 0;
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&maps.first_k);
         tma_prefetch_desc(KIND <= POLY ? &maps.second_k : &maps.second_mn);
@@ -336,67 +391,73 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
                 mbar_expect_tx(bar, C::STAGE);
                 for (int part = 0; part < 1 + C::FL; ++part, dst += OPB) {
                     if (KIND == GRAM)
-                        tma_load_3d(dst, &maps.first_k, k, bi * TM, 2 * u + part, bar);
+                        tma_load_3d(dst, &maps.first_k, k, i0, 2 * u + part, bar);
                     else
-                        load_symmetric(dst, &maps.first_k, &maps.first_mn, bi, k, 2 * u + part, bar);
+                        load_symmetric(dst, &maps.first_k, &maps.first_mn, i0, TM, k, 2 * u + part, bar);
                 }
-                for (int part = 0; part < 1 + C::SL; ++part, dst += OPB) {
+                for (int part = 0; part < 1 + C::SL; ++part, dst += C::SECOND) {
                     if (KIND == GRAM) {
-                        tma_load_3d(dst, &maps.second_k, k, bj * TM, 2 * u + part, bar);
+                        tma_load_3d(dst, &maps.second_k, k, j0, 2 * u + part, bar);
                     } else if (KIND == POLY) {
-                        load_symmetric(dst, &maps.second_k, &maps.second_mn, bj, k, 2 * u + part, bar);
+                        load_symmetric(dst, &maps.second_k, &maps.second_mn, j0, C::BN, k, 2 * u + part, bar);
                     } else {
-                        tma_load_3d(dst, &maps.second_mn, bj * TM, k, 2 * u + part, bar);
-                        tma_load_3d(dst + OPB / 2, &maps.second_mn, bj * TM + 64, k, 2 * u + part, bar);
+                        for (int c = 0; c < C::BN; c += 64)
+                            tma_load_3d(dst + c / 64 * PANEL, &maps.second_mn, j0 + c, k, 2 * u + part, bar);
                     }
                 }
             }
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            int last = -1;  // the hi hi accumulator in use
+            int acc = 0, count = 0;  // the hi hi accumulator in use, and its MMAs so far
             for (int i = 0; i < nk; ++i) {
                 const int slot = i % C::STAGES, t = (k0 + i) * KB / TM;
                 mbar_wait(&bars->full[slot], (i / C::STAGES) & 1, TTT_DEVERR_TIMEOUT_TMA);
                 tc::fence_after();
-                const int fm = KIND != GRAM && t < bi, sm = KIND >= NEXT || (KIND == POLY && t < bj);  // MN-major
+                const int fm = KIND != GRAM && t < bi, sm = KIND >= NEXT || (KIND == POLY && t < j0 / TM);  // MN-major
                 const uint32_t fb = smem_u32(ring + slot * C::STAGE), sb = fb + (1 + C::FL) * OPB;
-                const uint64_t fh = tc::smem_desc(fb, fm ? OPB / 2 : 16, 1024, 2), sh = tc::smem_desc(sb, sm ? OPB / 2 : 16, 1024, 2);
-                const uint64_t lo = OPB >> 4, fstep = fm ? 128 : 2, sstep = sm ? 128 : 2;
-                const uint32_t idesc = tc::idesc_f16(128, 128, 0, 0) | (uint32_t)fm << 15 | (uint32_t)sm << 16;
-                const int acc = i * C::ACC / nk;
-                const uint32_t to = tmem + acc * TM, cross = tmem + C::ACC * TM;
+                const uint64_t fh = tc::smem_desc(fb, fm ? PANEL : 16, 1024, 2), sh = tc::smem_desc(sb, sm ? PANEL : 16, 1024, 2);
+                const uint64_t fstep = fm ? 128 : 2, sstep = sm ? 128 : 2;
+                const uint32_t idesc = tc::idesc_f16(TM, C::BN, 0, 0) | (uint32_t)fm << 15 | (uint32_t)sm << 16;
+                const uint32_t cross = tmem + C::ACC * C::BN;
 #pragma unroll
                 for (int ks = 0; ks < KB / 16; ++ks) {
                     const uint64_t f = fh + fstep * ks, s = sh + sstep * ks;
-                    tc::mma_bf16(to, f, s, idesc, acc == last);
-                    last = acc;
-                    if (C::SL) tc::mma_bf16(cross, f, s + lo, idesc, i > 0 || ks > 0);
-                    if (C::FL) tc::mma_bf16(cross, f + lo, s, idesc, C::SL || i > 0 || ks > 0);
+                    if (count == len) {
+                        ++acc;
+                        count = 0;
+                    }
+                    tc::mma_bf16(tmem + acc * C::BN, f, s, idesc, count++ > 0);
+                    if (C::SL) tc::mma_bf16(cross, f, s + (C::SECOND >> 4), idesc, i > 0 || ks > 0);
+                    if (C::FL) tc::mma_bf16(cross, f + (OPB >> 4), s, idesc, C::SL || i > 0 || ks > 0);
                 }
                 tc::commit(&bars->empty[slot]);
             }
             tc::commit(&bars->done);
         }
     }
-    // Epilogue: two groups of four warps, group g taking columns 64 g .. 64 g + 63; a warp reads the 32
-    // lanes (rows) of its quarter of tensor memory.
+    // Epilogue: two groups of four warps, each taking half of the columns; a warp reads the 32 lanes (rows)
+    // of its quarter of tensor memory.
+    constexpr int HALF = C::BN / 2;
     const int g = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127, row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int used = nk > 0 ? (nk - 1) * C::ACC / nk + 1 : 0;
     // columns c .. c + 15 of the accumulators' sum, in the thread's row
     auto take = [&](int c, float (&v)[16]) {
-        float x[C::ACCS][16];
 #pragma unroll
-        for (int a = 0; a < C::ACCS; ++a) tc::ld16(lane_base + a * TM + c, x[a]);
-        tc::wait_ld();
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = C::FL || C::SL ? (used > 0 ? x[C::ACC][e] : 0.f) : 0.f;
+        for (int a0 = 0; a0 < C::ACCS; a0 += 4) {  // four accumulators' loads in flight
+            float x[4][16];
 #pragma unroll
-        for (int a = 0; a < C::ACC; ++a)
-            if (a < used)
+            for (int a = 0; a < 4; ++a)
+                if (a0 + a < C::ACCS) tc::ld16(lane_base + (a0 + a) * C::BN + c, x[a]);
+            tc::wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += x[a][e];
+            for (int a = 0; a < 4; ++a)
+                if (a0 + a < used || (a0 + a == C::ACC && used > 0))
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] += a0 + a < C::ACCS ? x[a][e] : 0.f;
+        }
     };
     if (warp >= 2) {
         if (nk > 0) {
@@ -406,30 +467,30 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
         if (S == 1) {
             uint8_t* area = ring + g * stage_area(TM);
 #pragma unroll 1
-            for (int c0 = 64 * g; c0 < 64 * g + 64; c0 += 32) {
+            for (int c0 = HALF * g; c0 < HALF * g + HALF; c0 += 32) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 16) {
                     float v[16];
                     take(c0 + c, v);
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
-                        stage4<KIND>(p, bi * TM + row, bj * TM + c0 + c + e, area, TM, row, c + e, {v[e], v[e + 1], v[e + 2], v[e + 3]});
+                        stage4<KIND>(p, i0 + row, j0 + c0 + c + e, area, TM, row, c + e, {v[e], v[e + 1], v[e + 2], v[e + 3]});
                 }
                 group_sync(g);
-                flush32<KIND, TM>(p, u, bi * TM, bj * TM + c0, area, tid);
+                flush32<KIND, TM>(p, u, i0, j0 + c0, area, tid);
                 group_sync(g);
             }
         }
     }
-    if (S > 1) {
+    if (C::EXCHANGE > 0 && S > 1) {
         const int R = TM / S;                          // rows of a slice
-        float* buf = reinterpret_cast<float*>(ring);   // [S][128 columns][R], over the ring
+        float* buf = reinterpret_cast<float*>(ring);   // [S][BN columns][R], over the ring
         cluster_sync_all();  // every CTA's MMAs have read their operands: the rings are free
         if (warp >= 2) {
-            float* here = buf + r * TM * R + row % R;
+            float* here = buf + r * C::BN * R + row % R;
             const uint32_t there = dsmem_map(here, row / R);
 #pragma unroll 1
-            for (int c = 64 * g; c < 64 * g + 64; c += 16) {
+            for (int c = HALF * g; c < HALF * g + HALF; c += 16) {
                 float v[16];
                 take(c, v);
                 if (row / R == r)
@@ -443,13 +504,13 @@ __global__ void __launch_bounds__(THREADS, C::MINB) product_kernel(const __grid_
         }
         cluster_sync_all();
         if (warp >= 2) {
-            const int row0 = bi * TM + r * R, col0 = bj * TM + 64 * g;
+            const int row0 = i0 + r * R, col0 = j0 + HALF * g;
             if (S == 2)
-                finish_slice<KIND, 2>(p, u, row0, col0, buf, ring + EXCHANGE, g, tid);
+                finish_slice<KIND, C::BN, 2>(p, u, row0, col0, buf, ring + C::EXCHANGE, g, tid);
             else if (S == 4)
-                finish_slice<KIND, 4>(p, u, row0, col0, buf, ring + EXCHANGE, g, tid);
+                finish_slice<KIND, C::BN, 4>(p, u, row0, col0, buf, ring + C::EXCHANGE, g, tid);
             else
-                finish_slice<KIND, 8>(p, u, row0, col0, buf, ring + EXCHANGE, g, tid);
+                finish_slice<KIND, C::BN, 8>(p, u, row0, col0, buf, ring + C::EXCHANGE, g, tid);
         }
     }
     tc::fence_before();

@@ -911,7 +911,7 @@ OrthPlan orth_plan(long long U, int m, int n) {
     p.ldx = (p.N + 7) / 8 * 8;
     p.lda = (p.M + 7) / 8 * 8;
     const long long mn = (long long)m * n;
-    p.parts = (int)std::min<long long>(orth::MAX_PARTS, (mn + 4095) / 4096);
+    p.parts = (int)std::min<long long>(orth::MAX_PARTS, (mn + 8191) / 8192);
     p.part = 0;
     p.x = align256((size_t)U * p.parts * 8);
     p.z = p.x + align256((size_t)U * p.M * p.ldx * 4);
@@ -927,27 +927,35 @@ int orth_check(int steps, float a, float b, float c, float eps) {
         return TTT_ERR_INVALID_ARG;
     return orth_coef_ok(a, b, c, steps) ? TTT_OK : TTT_ERR_UNSUPPORTED;
 }
-// The split of K over a cluster that is fastest by count: a K block's MMAs take 67 cycles per 128 x 128 x
-// 16 (four per product), a tile's start and end about 4500 and the exchange about 3500, and 148 SMs hold
-// 148, 72, 33 or 15 clusters of 1, 2, 4 or 8.  (384 x 1536: X X^T, 24 blocks and 6 tiles, 8 ways; P X, 6
-// blocks and 36 tiles, not at all.)  Full precision takes no more than 16 K blocks in an accumulator chain
-// where it can.
+// A product's tile width and split of K over a cluster, the fastest by count: K blocks at their cycles
+// (Config::BLOCK), a tile's start and end about 3000 and 35 a column (7 more accumulators: as much again),
+// the exchange of a split tile about 2000 and 20 a column, and 148 SMs holding 148, 72, 33 or 15 clusters of
+// 1, 2, 4 or 8.  Full precision takes no more than 50 MMAs into one accumulator where it can.
+struct OrthPick {
+    int bn = 0, S = 0;
+    long long cycles = 0;
+};
+int orth_tiles(bool symmetric, int M, int cols, int bn) {
+    const int tm = (M + orth::TM - 1) / orth::TM, tn = (cols + bn - 1) / bn;
+    if (!symmetric) return tm * tn;
+    int t = 0;
+    for (int i = 0; i < tm; ++i) t += tn - i * orth::TM / bn;
+    return t;
+}
 template <typename C>
-int orth_split(long long tiles, int kblocks) {
+void orth_consider(OrthPick& best, int tiles, long long U, int kblocks) {
     const int room[4] = {148, 72, 33, 15};
-    const long long block = 4 * 67 * (1 + C::FL + C::SL);
-    int best = 1;
-    long long least = 0;
-    for (int i = 0, S = 1; i < 4; ++i, S *= 2) {
+    for (int i = 0, S = 1; i < (C::EXCHANGE ? 4 : 1); ++i, S *= 2) {
         if (S > 1 && kblocks < 2 * S) break;
-        const long long per = (kblocks + S - 1) / S, waves = (tiles + room[i] * C::MINB - 1) / (room[i] * C::MINB);
-        const long long cycles = waves * (per * block * C::MINB + 4500 + (S > 1 ? 3500 : 0));
-        if (i == 0 || cycles < least || (C::ACC > 1 && (kblocks + best - 1) / best > 16)) {
-            best = S;
-            least = cycles;
+        const long long per = (kblocks + S - 1) / S, waves = (tiles * U + room[i] - 1) / room[i];
+        long long cycles = waves * (per * C::BLOCK + 3000 + 35 * C::BN + (S > 1 ? 2000 + 20 * C::BN : 0));
+        if (C::FL && per * 4 > 50 * C::ACC) cycles *= 2;
+        if (!best.bn || cycles < best.cycles) {
+            best.bn = C::BN;
+            best.S = S;
+            best.cycles = cycles;
         }
     }
-    return best;
 }
 template <int K>
 using Kind = std::integral_constant<int, K>;
@@ -970,55 +978,77 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
             return rc;
         return launched(1);
     }
-    const int tm = (p.M + orth::TM - 1) / orth::TM, tn = (p.N + orth::TM - 1) / orth::TM;
-    if (orth::Full::SMEM > dev->smem_optin || tm * tn > 65535) return TTT_ERR_UNSUPPORTED;
+    if (orth_tiles(false, p.M, p.N, 64) > 65535) return TTT_ERR_UNSUPPORTED;
+    constexpr bool kHalf = sizeof(T) == 2;  // bf16: X and P are held in one fp16 number
     const long long mn = (long long)m * n;
     char* w = static_cast<char*>(workspace);
     double* part = reinterpret_cast<double*>(w + p.part);
     __half *X = reinterpret_cast<__half*>(w + p.x), *Z = reinterpret_cast<__half*>(w + p.z);
     __half *A = reinterpret_cast<__half*>(w + p.a), *Q = reinterpret_cast<__half*>(w + p.q), *P = reinterpret_cast<__half*>(w + p.p);
-    auto maps = [&](__half* y, int ld, CUtensorMap* k, CUtensorMap* mn_map) {
-        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-        const CUtensorMapDataType f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-        return tmap_bf16_box(k, y, ld, p.M, (int)U * 2, orth::KB, orth::TM, sw, f16) &&
-               tmap_bf16_box(mn_map, y, ld, p.M, (int)U * 2, 64, orth::KB, sw, f16);
+
+    // the three products' tiles
+    const int kx = (p.N + orth::KB - 1) / orth::KB, km = (p.M + orth::KB - 1) / orth::KB;
+    OrthPick pick[3];
+    auto consider = [&](auto bn) {
+        constexpr int BN = bn();
+        using C = std::conditional_t<kHalf, orth::High<BN>, orth::Full<BN>>;
+        if constexpr (BN <= 128) {
+            orth_consider<C>(pick[0], orth_tiles(true, p.M, p.M, BN), U, kx);
+            orth_consider<orth::Full<BN>>(pick[1], orth_tiles(true, p.M, p.M, BN), U, km);
+        }
+        if constexpr (BN <= 128 || kHalf) orth_consider<C>(pick[2], orth_tiles(false, p.M, p.N, BN), U, km);
     };
-    orth::Maps gram[2], poly, next[2];  // [1]: X is in Z
+    consider(std::integral_constant<int, 64>());
+    consider(std::integral_constant<int, 128>());
+    consider(std::integral_constant<int, 256>());
+
+    auto map = [&](CUtensorMap* t, __half* y, int ld, int box_cols, int box_rows) {
+        return tmap_bf16_box(t, y, ld, p.M, (int)U * 2, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+    };
+    orth::Maps gram[2] = {}, poly = {}, next[2] = {};  // [1]: X is in Z
     for (int t = 0; t < 2; ++t) {
-        if (!maps(t ? Z : X, p.ldx, &gram[t].first_k, &gram[t].first_mn)) return TTT_ERR_CUDA;
-        gram[t].second_k = next[t].second_k = gram[t].first_k;
-        gram[t].second_mn = next[t].second_mn = gram[t].first_mn;
+        if (!map(&gram[t].first_k, t ? Z : X, p.ldx, orth::KB, orth::TM) ||
+            !map(&gram[t].second_k, t ? Z : X, p.ldx, orth::KB, pick[0].bn) ||
+            !map(&next[t].second_mn, t ? Z : X, p.ldx, 64, orth::KB))
+            return TTT_ERR_CUDA;
     }
-    if (!maps(A, p.lda, &poly.first_k, &poly.first_mn) || !maps(Q, p.lda, &poly.second_k, &poly.second_mn) ||
-        !maps(P, p.lda, &next[0].first_k, &next[0].first_mn))
+    if (!map(&poly.first_k, A, p.lda, orth::KB, orth::TM) || !map(&poly.first_mn, A, p.lda, 64, orth::KB) ||
+        !map(&poly.second_k, Q, p.lda, orth::KB, pick[1].bn) || !map(&poly.second_mn, Q, p.lda, 64, orth::KB) ||
+        !map(&next[0].first_k, P, p.lda, orth::KB, orth::TM) || !map(&next[0].first_mn, P, p.lda, 64, orth::KB))
         return TTT_ERR_CUDA;
     next[1].first_k = next[0].first_k;
     next[1].first_mn = next[0].first_mn;
-    constexpr bool kHalf = sizeof(T) == 2;  // bf16: X is held in one fp16 number
-    using GramC = std::conditional_t<kHalf, orth::High, orth::Full>;
-    using NextC = std::conditional_t<kHalf, orth::Left, orth::Full>;
+
     if (int rc = launch_pdl(orth::square_kernel<T>, dim3((unsigned)p.parts, (unsigned)U), orth::TPB, 0, st, x, part, mn))
         return rc;
-    if (int rc = launch_pdl(orth::start_kernel<T>, dim3((p.ldx + 31) / 32, (p.M + 31) / 32, (unsigned)U), 256, 0, st, x,
-                            (const double*)part, X, p.parts, p.M, p.N, p.ldx, p.tall, kHalf ? 1 : 2, eps))
+    if (!p.tall && p.N % 8 == 0) {
+        if (int rc = launch_pdl(orth::start8_kernel<T>, dim3((unsigned)((mn / 8 + 255) / 256), (unsigned)U), 256, 0, st, x,
+                                (const double*)part, X, p.parts, mn, kHalf ? 1 : 2, eps))
+            return rc;
+    } else if (int rc = launch_pdl(orth::start_kernel<T>, dim3((p.ldx + 31) / 32, (p.M + 31) / 32, (unsigned)U), 256, 0, st, x,
+                                   (const double*)part, X, p.parts, p.M, p.N, p.ldx, p.tall, kHalf ? 1 : 2, eps)) {
         return rc;
-    auto product = [&](auto config, auto kind, const orth::Maps& maps, int tiles, int K, PParams q) {
+    }
+    PParams base = {};
+    base.M = p.M;
+    base.N = p.N;
+    base.tall = p.tall;
+    base.ca = a;
+    base.cb = b;
+    base.cc = c;
+    base.scale = scale;
+    base.out = out;
+    auto launch = [&](auto config, auto kind, const orth::Maps& maps, int S, PParams q) -> int {
         using C = decltype(config);
         const auto kern = orth::product_kernel<C, kind()>;
         static SmemRecord record;
-        if (!allow_smem(kern, C::SMEM, record)) return (int)TTT_ERR_CUDA;
-        q.kblocks = (K + orth::KB - 1) / orth::KB;
-        q.M = p.M;
-        q.N = p.N;
-        q.tall = p.tall;
-        q.tiles_n = tn;
-        q.ca = a;
-        q.cb = b;
-        q.cc = c;
-        q.scale = scale;
-        const int S = orth_split<C>((long long)tiles * U, q.kblocks);
+        if (!allow_smem(kern, C::SMEM, record)) return TTT_ERR_CUDA;
+        const int cols = kind() <= orth::POLY ? p.M : p.N;
+        q.kblocks = kind() == orth::GRAM ? kx : km;
+        q.tiles_n = (cols + C::BN - 1) / C::BN;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)S, (unsigned)tiles, (unsigned)U);
+        cfg.gridDim = dim3((unsigned)S, (unsigned)orth_tiles(kind() <= orth::POLY, p.M, cols, C::BN), (unsigned)U);
         cfg.blockDim = dim3(orth::THREADS, 1, 1);
         cfg.dynamicSmemBytes = C::SMEM;
         cfg.stream = st;
@@ -1031,24 +1061,34 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, kern, maps, q) == cudaSuccess ? (int)TTT_OK : (int)TTT_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, kern, maps, q) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
     };
+    // full: the product takes lo parts too
+    auto product = [&](auto full, auto kind, const orth::Maps& maps, const OrthPick& k, const PParams& q) -> int {
+        if constexpr (full()) {
+            return k.bn == 64 ? launch(orth::Full<64>(), kind, maps, k.S, q) : launch(orth::Full<128>(), kind, maps, k.S, q);
+        } else {
+            if constexpr (kind() >= orth::NEXT)
+                if (k.bn == 256) return launch(orth::High<256>(), kind, maps, k.S, q);
+            return k.bn == 64 ? launch(orth::High<64>(), kind, maps, k.S, q) : launch(orth::High<128>(), kind, maps, k.S, q);
+        }
+    };
+    constexpr std::bool_constant<!kHalf> rest;
     for (int k = 0; k < steps; ++k) {
         const bool odd = k & 1, last = k + 1 == steps;
-        PParams q = {};
+        PParams q = base;
         q.parts = 2;
         q.y = A;
         q.y2 = Q;
         q.ld = p.lda;
-        if (int rc = product(GramC(), Kind<orth::GRAM>(), gram[odd], tm * (tm + 1) / 2, p.N, q)) return rc;
-        q.y = P;
-        if (int rc = product(orth::Full(), Kind<orth::POLY>(), poly, tm * (tm + 1) / 2, p.M, q)) return rc;
+        if (int rc = product(rest, Kind<orth::GRAM>(), gram[odd], pick[0], q)) return rc;
         q.parts = kHalf ? 1 : 2;
+        q.y = P;
+        if (int rc = product(std::true_type(), Kind<orth::POLY>(), poly, pick[1], q)) return rc;
         q.y = odd ? X : Z;
         q.ld = p.ldx;
-        q.out = out;
-        const int rc = last ? product(NextC(), Kind<kHalf ? orth::OUT_BF16 : orth::OUT_F32>(), next[odd], tm * tn, p.M, q)
-                            : product(NextC(), Kind<orth::NEXT>(), next[odd], tm * tn, p.M, q);
+        const int rc = last ? product(rest, Kind<kHalf ? orth::OUT_BF16 : orth::OUT_F32>(), next[odd], pick[2], q)
+                            : product(rest, Kind<orth::NEXT>(), next[odd], pick[2], q);
         if (rc) return rc;
     }
     return launched(2 + 3 * steps);
