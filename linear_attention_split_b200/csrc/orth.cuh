@@ -20,7 +20,7 @@
 // product_kernel: one tile of 128 x 64, 128 or 256 of a product per cluster; the K range is split over the S
 // CTAs of the cluster when there are few tiles, and the partial tiles are exchanged through
 // distributed shared memory (each CTA adds one slice of rows, in rank order: deterministic).  Per CTA
-// a TMA producer and a tcgen05 issuer over a ring of 64-wide K blocks, and four epilogue warps, which
+// a TMA producer and two tcgen05 issuers over a ring of 64-wide K blocks, and eight epilogue warps, which
 // stage what they write so that rows go out whole (straight from the accumulator's layout, one row per
 // lane, a tile took 5300 cycles; staged about a third).  A, Q and P are symmetric: only tiles on or
 // above the diagonal are formed, and an operand block below it is read from its mirror image as an
@@ -157,7 +157,6 @@ constexpr int TM = 128, KB = 64;                     // rows of a tile of the ou
 constexpr int PANEL = 64 * KB * 2;                   // a K block of 64 rows or columns, 8 KB
 constexpr int OPB = 2 * PANEL;                       // the first operand's K block
 constexpr int MAX_SPLIT = 8;
-constexpr int THREADS = 64 + 256;                    // producer, issuer, eight epilogue warps
 constexpr float SQ = 512.f;                          // scale of stored Q
 
 enum Kind { GRAM = 0, POLY = 1, NEXT = 2, OUT_F32 = 3, OUT_BF16 = 4 };
@@ -188,7 +187,11 @@ struct Config {
     static constexpr int BN = BN_, ACC = ACC_, STAGES = STAGES_;
     static constexpr int SECOND = BN / 64 * PANEL;                 // the second operand's K block
     static constexpr int STAGE = (1 + FL) * OPB + (1 + SL) * SECOND;
-    static constexpr int ACCS = ACC + (FL || SL);
+    static constexpr bool CROSS = FL || SL;
+    static constexpr int ACCS = ACC + CROSS;
+    static constexpr int ISSUERS = CROSS ? 1 : 2;
+    static constexpr int FRONT = 32 * (1 + ISSUERS), THREADS = FRONT + 256;  // producer, issuers; eight epilogue warps
+    static_assert(CROSS || ACC == ISSUERS, "hi hi alone: one accumulator for each issuer");
     static constexpr int COLS = ACCS * BN;                         // of tensor memory
     static constexpr int EXCHANGE = BN > 128 ? 0 : TM * BN * 4;    // the S partial slices of a tile
     // the ring; over it the exchange and what is staged
@@ -205,7 +208,7 @@ struct Config {
 template <int BN>
 using Full = Config<true, true, BN, BN == 64 ? 7 : 3, BN == 64 ? 4 : 3>;
 template <int BN>
-using High = Config<false, false, BN, 1, BN == 64 ? 8 : BN == 128 ? 6 : 4>;
+using High = Config<false, false, BN, 2, BN == 64 ? 8 : BN == 128 ? 6 : 4>;
 
 __device__ __forceinline__ void group_sync(int g) {
     if (g == 0)
@@ -346,7 +349,7 @@ struct Maps {
     CUtensorMap first_k, first_mn, second_k, second_mn;
 };
 template <typename C, int KIND>
-__global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ Maps maps, const PParams p) {
+__global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_constant__ Maps maps, const PParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_align<1024>(smem_raw);
     PBars* bars = reinterpret_cast<PBars*>(ring + C::RING);
@@ -360,8 +363,10 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     }
     const int i0 = bi * TM, j0 = bj * C::BN;  // the tile's place
     const int per = (p.kblocks + S - 1) / S, k0 = min(r * per, p.kblocks), nk = min(per, p.kblocks - k0);
-    // accumulators for hi hi: `used` of them, each for a run of `len` of the 4 nk MMAs
-    const int len = (4 * nk + C::ACC - 1) / C::ACC, used = nk > 0 ? (4 * nk + len - 1) / len : 0;
+    // accumulators for hi hi: `used` of them, each for a run of `len` of the 4 nk MMAs (hi hi alone: one for
+    // each issuer)
+    const int len = (4 * nk + C::ACC - 1) / C::ACC;
+    const int used = !C::CROSS ? min(nk, 2) : nk > 0 ? (4 * nk + len - 1) / len : 0;
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&maps.first_k);
         tma_prefetch_desc(KIND <= POLY ? &maps.second_k : &maps.second_mn);
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 1);
         }
-        mbar_init(&bars->done, 1);
+        mbar_init(&bars->done, C::ISSUERS);
         mbar_fence_init();
     }
     if (warp == 1) tc::alloc(&bars->tmem_base, C::COLS);
@@ -380,6 +385,43 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     griddep_launch();
     const uint32_t tmem = bars->tmem_base;
 
+    // The MMAs of one issuing thread.  One thread spends about 300 cycles a K block on its barriers (a test of a
+    // phase that is over already takes 200) while the tensor cores wait.  The four MMAs of hi hi alone are too
+    // short to cover that: two issuers take alternate K blocks there, each with an accumulator of its own, so
+    // that nothing depends on how they interleave (1024 x 4096 bf16 180 -> 165 us).  Twelve MMAs are faster from
+    // one thread (384 x 1536 fp32 101 us; hi hi and cross terms from two threads 110).  The issuer's number is a
+    // constant: addresses that come from the thread's index cost a move to the uniform registers for each MMA.
+    auto issue = [&](auto issuer) {
+        constexpr int j = decltype(issuer)::value;
+        int acc = j, count = 0;  // the hi hi accumulator in use, and its MMAs so far
+        bool ready = false;
+        for (int i = j; i < nk; i += C::ISSUERS) {
+            const int slot = i % C::STAGES, t = (k0 + i) * KB / TM;
+            if (!ready) mbar_wait(&bars->full[slot], (i / C::STAGES) & 1, TTT_DEVERR_TIMEOUT_TMA);
+            const int n = i + C::ISSUERS;  // the next block's phase is asked for ahead of this block's MMAs
+            ready = n < nk && mbar_test_wait(&bars->full[n % C::STAGES], (n / C::STAGES) & 1);
+            tc::fence_after();
+            const int fm = KIND != GRAM && t < bi, sm = KIND >= NEXT || (KIND == POLY && t < j0 / TM);  // MN-major
+            const uint32_t fb = smem_u32(ring + slot * C::STAGE), sb = fb + (1 + C::FL) * OPB;
+            const uint64_t fh = tc::smem_desc(fb, fm ? PANEL : 16, 1024, 2), sh = tc::smem_desc(sb, sm ? PANEL : 16, 1024, 2);
+            const uint64_t fstep = fm ? 128 : 2, sstep = sm ? 128 : 2;
+            const uint32_t idesc = tc::idesc_f16(TM, C::BN, 0, 0) | (uint32_t)fm << 15 | (uint32_t)sm << 16;
+            const uint32_t cross = tmem + C::ACC * C::BN;
+#pragma unroll
+            for (int ks = 0; ks < KB / 16; ++ks) {
+                const uint64_t f = fh + fstep * ks, s = sh + sstep * ks;
+                if (C::CROSS && count == len) {
+                    ++acc;
+                    count = 0;
+                }
+                tc::mma_bf16(tmem + acc * C::BN, f, s, idesc, count++ > 0);
+                if (C::SL) tc::mma_bf16(cross, f, s + (C::SECOND >> 4), idesc, i > 0 || ks > 0);
+                if (C::FL) tc::mma_bf16(cross, f + (OPB >> 4), s, idesc, C::SL || i > 0 || ks > 0);
+            }
+            tc::commit(&bars->empty[slot]);
+        }
+        tc::commit(&bars->done);
+    };
     if (warp == 0) {
         if (lane == 0) {
             for (int i = 0; i < nk; ++i) {
@@ -408,38 +450,15 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int acc = 0, count = 0;  // the hi hi accumulator in use, and its MMAs so far
-            for (int i = 0; i < nk; ++i) {
-                const int slot = i % C::STAGES, t = (k0 + i) * KB / TM;
-                mbar_wait(&bars->full[slot], (i / C::STAGES) & 1, TTT_DEVERR_TIMEOUT_TMA);
-                tc::fence_after();
-                const int fm = KIND != GRAM && t < bi, sm = KIND >= NEXT || (KIND == POLY && t < j0 / TM);  // MN-major
-                const uint32_t fb = smem_u32(ring + slot * C::STAGE), sb = fb + (1 + C::FL) * OPB;
-                const uint64_t fh = tc::smem_desc(fb, fm ? PANEL : 16, 1024, 2), sh = tc::smem_desc(sb, sm ? PANEL : 16, 1024, 2);
-                const uint64_t fstep = fm ? 128 : 2, sstep = sm ? 128 : 2;
-                const uint32_t idesc = tc::idesc_f16(TM, C::BN, 0, 0) | (uint32_t)fm << 15 | (uint32_t)sm << 16;
-                const uint32_t cross = tmem + C::ACC * C::BN;
-#pragma unroll
-                for (int ks = 0; ks < KB / 16; ++ks) {
-                    const uint64_t f = fh + fstep * ks, s = sh + sstep * ks;
-                    if (count == len) {
-                        ++acc;
-                        count = 0;
-                    }
-                    tc::mma_bf16(tmem + acc * C::BN, f, s, idesc, count++ > 0);
-                    if (C::SL) tc::mma_bf16(cross, f, s + (C::SECOND >> 4), idesc, i > 0 || ks > 0);
-                    if (C::FL) tc::mma_bf16(cross, f + (OPB >> 4), s, idesc, C::SL || i > 0 || ks > 0);
-                }
-                tc::commit(&bars->empty[slot]);
-            }
-            tc::commit(&bars->done);
-        }
+        if (lane == 0) issue(std::integral_constant<int, 0>());
+    } else if (C::ISSUERS > 1 && warp == 2) {
+        if (lane == 0) issue(std::integral_constant<int, 1>());
     }
     // Epilogue: two groups of four warps, each taking half of the columns; a warp reads the 32 lanes (rows)
     // of its quarter of tensor memory.
     constexpr int HALF = C::BN / 2;
-    const int g = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127, row = (warp & 3) * 32 + lane;
+    constexpr int FIRST = C::FRONT / 32;  // epilogue warp
+    const int g = (warp - FIRST) >> 2, tid = (threadIdx.x - C::FRONT) & 127, row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     // columns c .. c + 15 of the accumulators' sum, in the thread's row
     auto take = [&](int c, float (&v)[16]) {
@@ -454,12 +473,12 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             tc::wait_ld();
 #pragma unroll
             for (int a = 0; a < 4; ++a)
-                if (a0 + a < used || (a0 + a == C::ACC && used > 0))
+                if (a0 + a < used || (C::CROSS && a0 + a == C::ACC && used > 0))
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] += a0 + a < C::ACCS ? x[a][e] : 0.f;
         }
     };
-    if (warp >= 2) {
+    if (warp >= FIRST) {
         if (nk > 0) {
             mbar_wait(&bars->done, 0, TTT_DEVERR_TIMEOUT_TMA);
             tc::fence_after();
@@ -486,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         const int R = TM / S;                          // rows of a slice
         float* buf = reinterpret_cast<float*>(ring);   // [S][BN columns][R], over the ring
         cluster_sync_all();  // every CTA's MMAs have read their operands: the rings are free
-        if (warp >= 2) {
+        if (warp >= FIRST) {
             float* here = buf + r * C::BN * R + row % R;
             const uint32_t there = dsmem_map(here, row / R);
 #pragma unroll 1
@@ -503,7 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
             }
         }
         cluster_sync_all();
-        if (warp >= 2) {
+        if (warp >= FIRST) {
             const int row0 = i0 + r * R, col0 = j0 + HALF * g;
             if (S == 2)
                 finish_slice<KIND, C::BN, 2>(p, u, row0, col0, buf, ring + C::EXCHANGE, g, tid);

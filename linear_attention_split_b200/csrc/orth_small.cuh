@@ -200,7 +200,7 @@ constexpr int D = 64, DD = D * D, ROWB = 128, TILE = TM * ROWB;
 
 // G and C^T of one split of a unit's tokens, bf16, d = 64: [V | K]^T K on the tcgen05 tensor cores.
 // Grid (S, U); part [U][S][2][64][64] (G, C^T).
-constexpr int G_STAGES = 3;
+constexpr int G_STAGES = 3, G_THREADS = 64 + 128;  // producer, issuer, four epilogue warps
 constexpr uint32_t IDESC_GRAM = tc::idesc_bf16(128, 64, 1, 1);
 struct GBars {
     uint64_t full[G_STAGES], empty[G_STAGES], done;
@@ -208,7 +208,7 @@ struct GBars {
 };
 constexpr int g_smem_bytes() { return G_STAGES * 2 * TILE + (int)sizeof(GBars) + 1024; }
 
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(G_THREADS)
     gram_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k, float* __restrict__ part,
                    int TT, int n_tiles) {
     extern __shared__ uint8_t smem_raw[];

@@ -1049,7 +1049,7 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         q.tiles_n = (cols + C::BN - 1) / C::BN;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)S, (unsigned)orth_tiles(kind() <= orth::POLY, p.M, cols, C::BN), (unsigned)U);
-        cfg.blockDim = dim3(orth::THREADS, 1, 1);
+        cfg.blockDim = dim3(C::THREADS, 1, 1);
         cfg.dynamicSmemBytes = C::SMEM;
         cfg.stream = st;
         cudaLaunchAttribute attr[2];
@@ -1141,7 +1141,7 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
         if (!tmap_bf16_3d(&tk, k, 64, N, (int)U, p.TT, sw) || !tmap_bf16_3d(&tv, v, 64, N, (int)U, p.TT, sw)) return TTT_ERR_CUDA;
         static SmemRecord record;
         if (!allow_smem(orth::gram_tc_kernel, orth::g_smem_bytes(), record)) return TTT_ERR_CUDA;
-        if (int rc = launch_pdl(orth::gram_tc_kernel, dim3((unsigned)p.S, (unsigned)U), orth::THREADS, orth::g_smem_bytes(), st, tv,
+        if (int rc = launch_pdl(orth::gram_tc_kernel, dim3((unsigned)p.S, (unsigned)U), orth::G_THREADS, orth::g_smem_bytes(), st, tv,
                                 tk, part, p.TT, p.n_tiles))
             return rc;
     } else {
