@@ -2,12 +2,15 @@
 // step whose inner update is orthogonalised (its gradient, its update, the general output pass).
 //
 // A matrix of at most 64 rows stays in shared memory through all steps, so nothing but the input and
-// the result touches HBM and a step costs three products of 64 x 64 x 64 (more along a long side)
-// with a block barrier after each: the chain of launches of orth.cuh costs 4 to 5 us a product.  The
-// operands are hi + lo fp16 as there; at this size the warp-level mma is the faster one (a tcgen05
-// product of one 64 x 64 tile spends most of its time on the way into and out of tensor memory).
-// The cross terms hi lo + lo hi have an accumulator of their own: the tensor cores drop the bits
-// below the accumulator's last at every addition, and shorter chains keep that below fp32 rounding.
+// the result touches HBM.  Each operand lies there as 128 rows, 64 of hi and 64 of lo (fp16, as in
+// orth.cuh), and one tcgen05 product of the stacked rows, [hi; lo] [hi | lo], gives hi hi, hi lo and
+// lo hi at once as quarters of a 128 x 128 accumulator: four MMAs of K = 16 for a 64 x 64 x 64 product,
+// 268 cycles.  lo hi sits in the lanes of the other two warps, so each half of the block sends the
+// other half's columns through shared memory and finishes 32 columns of 64 rows.
+//
+// The bound is latency: a step is three such products, each waiting for the one before (accumulator
+// out of tensor memory, exchange, rounding to hi + lo, operand written, MMAs).  48 KB of shared memory
+// and 128 columns of tensor memory let four blocks share an SM and fill one another's gaps.
 #pragma once
 #include "common.cuh"
 #include "orth.cuh"
@@ -16,137 +19,163 @@ namespace orth {
 
 constexpr int SM_M = 64;                 // rows of a small matrix
 constexpr int SM_N = 256;                // its longer side at most
-constexpr int SM_TPB = 256;              // 8 warps: 2 x 4 tiles of 32 x 16
-constexpr int SM_LD = SM_M + 8;          // padded row of A and P, in halves (16-byte rows, no bank conflicts)
-__host__ __device__ constexpr int sm_ldx(int N) { return (N + 63) / 64 * 64 + 8; }
-constexpr int SM_SQ = SM_M * SM_LD * 2;  // halves of A (hi and lo)
-constexpr int small_smem_bytes(int N) { return (2 * SM_SQ + SM_M * sm_ldx(N) * 2) * 2; }
+constexpr int SM_TPB = 128;
+constexpr int SM_OP = 2 * SM_M * 128;    // an operand of 64 columns: 64 rows of hi, 64 of lo, 128-byte swizzle
+constexpr int SM_EX = SM_M * SM_M * 4;   // the exchange
+struct SmallBars {
+    uint64_t done;
+    uint32_t tmem_base;
+    double sums[SM_TPB / 32];
+};
+__host__ __device__ constexpr int sm_strips(int N) { return (N + 63) / 64; }
+// X (a strip per 64 columns), A and P, the exchange
+constexpr int small_smem_bytes(int N) { return (sm_strips(N) + 1) * SM_OP + SM_EX + (int)sizeof(SmallBars) + 1024; }
+constexpr uint32_t SM_IDESC_K = tc::idesc_f16(128, 128, 0, 0), SM_IDESC_MN = tc::idesc_f16(128, 128, 0, 1);
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// 8 adjacent values into an operand at (row, col), col a multiple of 8
+__device__ __forceinline__ void put_op8(uint8_t* op, int row, int col, const float* v) {
+    uint2 h0, l0, h1, l1;
+    const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+    split4(a, h0, l0);
+    split4(b, h1, l1);
+    uint8_t* at = op + swz<3>((uint32_t)row * 128 + (uint32_t)col * 2);
+    *reinterpret_cast<uint4*>(at) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+    *reinterpret_cast<uint4*>(at + SM_M * 128) = make_uint4(l0.x, l0.y, l1.x, l1.y);
 }
 
-// A 32 x 16 tile of a product: rows row0.. of a ([64][lda], lo parts a_lo halves behind) times columns
-// col0.. of b, which is [n][k] (b symmetric or itself transposed) or, TRANS, [k][n].
-template <bool TRANS>
-__device__ __forceinline__ void tile_product(float (&acc)[2][2][4], const __half* a, int lda, int a_lo, int row0, const __half* b,
-                                             int ldb, int b_lo, int col0, int k16) {
-    const int lane = threadIdx.x & 31;
-    float low[2][2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = low[i][j][e] = 0.f;
-    const uint32_t pa = smem_u32(a + (row0 + (lane & 15)) * lda + (lane >> 4) * 8);
-    const uint32_t pb = TRANS ? smem_u32(b + (((lane >> 3) & 1) * 8 + (lane & 7)) * ldb + col0 + (lane >> 4) * 8)
-                              : smem_u32(b + (col0 + (lane >> 4) * 8 + (lane & 7)) * ldb + ((lane >> 3) & 1) * 8);
-    const uint32_t sb = TRANS ? 32u * ldb : 32u;  // bytes of 16 k
-#pragma unroll 4
-    for (int k = 0; k < k16; ++k) {
-        uint32_t ah[2][4], al[2][4], bh[4], bl[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t at = pa + 32u * i * lda + 32u * k;
-            ldsm_x4(at, ah[i][0], ah[i][1], ah[i][2], ah[i][3]);
-            ldsm_x4(at + 2u * a_lo, al[i][0], al[i][1], al[i][2], al[i][3]);
+// What a block of 128 threads works with
+struct Small {
+    uint8_t *X, *A;    // strips of X; A, then P
+    float* ex;
+    SmallBars* bars;
+    uint32_t tmem;
+    int products;      // products waited for so far (the barrier's phase)
+
+    __device__ __forceinline__ void begin(uint8_t* raw, int strips) {
+        X = smem_align<1024>(raw);
+        A = X + strips * SM_OP;
+        ex = reinterpret_cast<float*>(A + SM_OP);
+        bars = reinterpret_cast<SmallBars*>(A + SM_OP + SM_EX);
+        products = 0;
+        if (threadIdx.x == 0) {
+            mbar_init(&bars->done, 1);
+            mbar_fence_init();
         }
-        if (TRANS) {
-            ldsm_x4_t(pb + sb * k, bh[0], bh[1], bh[2], bh[3]);
-            ldsm_x4_t(pb + sb * k + 2u * b_lo, bl[0], bl[1], bl[2], bl[3]);
-        } else {
-            ldsm_x4(pb + sb * k, bh[0], bh[1], bh[2], bh[3]);
-            ldsm_x4(pb + sb * k + 2u * b_lo, bl[0], bl[1], bl[2], bl[3]);
-        }
+        if (threadIdx.x < 32) tc::alloc(&bars->tmem_base, 128);
+        tc::fence_before();
+        __syncthreads();
+        tc::fence_after();
+        tmem = bars->tmem_base;
+    }
+    __device__ __forceinline__ void end() {
+        tc::fence_before();
+        __syncthreads();
+        if (threadIdx.x < 32) tc::dealloc(tmem, 128);
+    }
+    // The operands that the block has written are seen by the tensor cores, and the accumulator has been read
+    __device__ __forceinline__ void written() {
+        fence_proxy_async_smem();
+        tc::fence_before();
+        __syncthreads();
+        tc::fence_after();
+    }
+    // v: columns 32 (warp / 2) .. + 31 of row 32 (warp % 2) + lane of hi hi + hi lo + lo hi
+    __device__ __forceinline__ void take(float (&v)[32]) {
+        mbar_wait<false>(&bars->done, products++ & 1, TTT_DEVERR_TIMEOUT_TMA);
+        tc::fence_after();
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 1) * 32 + lane;
+        const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16);
+        float s[32];
+        if (warp < 2) {
+            float h[32], l[32];
+            tc::ld16(at, v);
+            tc::ld16(at + 16, v + 16);
+            tc::ld16(at + 32, s);
+            tc::ld16(at + 48, s + 16);
+            tc::ld16(at + 64, h);
+            tc::ld16(at + 80, h + 16);
+            tc::ld16(at + 96, l);
+            tc::ld16(at + 112, l + 16);
+            tc::wait_ld();
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mma_f16(acc[i][j], ah[i], bh[2 * j], bh[2 * j + 1]);
-                mma_f16(low[i][j], ah[i], bl[2 * j], bl[2 * j + 1]);
-                mma_f16(low[i][j], al[i], bh[2 * j], bh[2 * j + 1]);
+            for (int c = 0; c < 32; ++c) {
+                v[c] += h[c];
+                s[c] += l[c];
             }
+        } else {
+            tc::ld16(at, s);
+            tc::ld16(at + 16, s + 16);
+            tc::ld16(at + 32, v);
+            tc::ld16(at + 48, v + 16);
+            tc::wait_ld();
+        }
+        float* out = ex + (warp < 2 ? 0 : 32 * SM_M) + row;  // [column][row]
+        const float* in = ex + (warp < 2 ? 32 * SM_M : 0) + row;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) out[c * SM_M] = s[c];
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] += in[c * SM_M];
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] += low[i][j][e];
-}
 
-__device__ __forceinline__ void put2(__half* hi, int lo, float x, float y) {
-    const __half2 h = __floats2half2_rn(x, y);
-    const float2 f = __half22float2(h);
-    *reinterpret_cast<__half2*>(hi) = h;
-    *reinterpret_cast<__half2*>(hi + lo) = __floats2half2_rn(x - f.x, y - f.y);
-}
-
-// All steps on X ([64][ldx] hi, then lo; zero outside the matrix) with A and P as scratch; the last
-// product goes to last(row, col, v, w): the values at (row, col) and (row, col + 1), times SX SP.
-// Enter with X written and not yet synchronised.
-template <typename Last>
-__device__ __forceinline__ void small_steps(__half* X, int ldx, __half* A, __half* P, int N, int steps, float ca, float cb,
-                                            float cc, Last last) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row0 = (warp & 1) * 32, col0 = (warp >> 1) * 16, gr = lane >> 2, gc = (lane & 3) * 2;
-    const int x_lo = SM_M * ldx, s_lo = SM_M * SM_LD, k16 = (N + 15) / 16, strips = (N + 63) / 64;
-    for (int step = 0; step < steps; ++step) {
-        float acc[2][2][4], a[2][2][4];
-        __syncthreads();  // X is written
-        tile_product<false>(acc, X, ldx, x_lo, row0, X, ldx, x_lo, col0, k16);
+    // All steps on X (written, not yet synchronised); the last product goes to last(row, column, v): 32 adjacent
+    // values of X, times SX SP.
+    template <typename Last>
+    __device__ __forceinline__ void steps(int strips, int count, float ca, float cb, float cc, Last last) {
+        const int warp = threadIdx.x >> 5, row = (warp & 1) * 32 + (threadIdx.x & 31), col = (warp >> 1) * 32;
+        const uint64_t xk = tc::smem_desc(smem_u32(X), 16, 1024, 2), xn = tc::smem_desc(smem_u32(X), SM_M * 128, 1024, 2);
+        const uint64_t ak = tc::smem_desc(smem_u32(A), 16, 1024, 2);
+        for (int k = 0; k < count; ++k) {
+            float v[32], a[32];
+            written();
+            if (threadIdx.x == 0) {
+                for (int s = 0; s < strips; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float v = acc[i][j][2 * h] * (1.f / SX), w = acc[i][j][2 * h + 1] * (1.f / SX);
-                    a[i][j][2 * h] = v;
-                    a[i][j][2 * h + 1] = w;
-                    put2(A + (row0 + 16 * i + 8 * h + gr) * SM_LD + col0 + 8 * j + gc, s_lo, v, w);
-                }
-        __syncthreads();  // A is written
-        tile_product<false>(acc, A, SM_LD, s_lo, row0, A, SM_LD, s_lo, col0, SM_M / 16);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = row0 + 16 * i + 8 * h + gr, c = col0 + 8 * j + gc;
-                    float v[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        v[e] = SP * (fmaf(cc / (SX * SX), acc[i][j][2 * h + e], cb / SX * a[i][j][2 * h + e]) +
-                                     (r == c + e ? ca : 0.f));
-                    put2(P + r * SM_LD + c, s_lo, v[0], v[1]);
-                }
-        __syncthreads();  // P is written
-        const bool done = step + 1 == steps;
-        for (int s = 0; s < strips; ++s) {
-            tile_product<true>(acc, P, SM_LD, s_lo, row0, X, ldx, x_lo, 64 * s + col0, SM_M / 16);
-            if (!done) __syncthreads();  // every warp has read this strip of X
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = row0 + 16 * i + 8 * h + gr, c = 64 * s + col0 + 8 * j + gc;
-                        if (done)
-                            last(r, c, acc[i][j][2 * h], acc[i][j][2 * h + 1]);
-                        else
-                            put2(X + r * ldx + c, x_lo, acc[i][j][2 * h] * (1.f / SP), acc[i][j][2 * h + 1] * (1.f / SP));
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t d = xk + (uint64_t)(s * (SM_OP >> 4) + 2 * ks);
+                        tc::mma_bf16(tmem, d, d, SM_IDESC_K, s > 0 || ks > 0);
                     }
+                tc::commit(&bars->done);
+            }
+            take(a);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) a[c] *= 1.f / SX;
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) put_op8(A, row, col + c, a + c);
+            written();
+            if (threadIdx.x == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) tc::mma_bf16(tmem, ak + 2 * ks, ak + 2 * ks, SM_IDESC_K, ks > 0);
+                tc::commit(&bars->done);
+            }
+            take(v);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                v[c] = SP * (fmaf(cc / (SX * SX), v[c], cb / SX * a[c]) + (row == col + c ? ca : 0.f));
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) put_op8(A, row, col + c, v + c);
+            const bool done = k + 1 == count;
+            for (int s = 0; s < strips; ++s) {
+                written();
+                if (threadIdx.x == 0) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        tc::mma_bf16(tmem, ak + 2 * ks, xn + (uint64_t)(s * (SM_OP >> 4) + 128 * ks), SM_IDESC_MN, ks > 0);
+                    tc::commit(&bars->done);
+                }
+                take(v);
+                if (done) {
+                    last(row, 64 * s + col, v);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] *= 1.f / SP;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8) put_op8(X + s * SM_OP, row, col + c, v + c);
+                }
+            }
         }
     }
-}
+};
 
 // sum over the block, in warp order
 __device__ __forceinline__ double block_sum(double s, double* sm) {
@@ -158,41 +187,42 @@ __device__ __forceinline__ double block_sum(double s, double* sm) {
     return s;
 }
 
-// one block per matrix: X [M][N] of the shorter side M <= 64, N <= 256
+// One block per matrix, X [M][N] with M <= 64, N <= 256.  Thread t holds row t % 64 and every second group
+// of 8 columns; a tall matrix is read along its rows, which are columns of X.
 template <typename T>
-__global__ void __launch_bounds__(SM_TPB, 2)
+__global__ void __launch_bounds__(SM_TPB, 3)
     small_kernel(const T* x, T* out, int M, int N, int tall, int steps, float ca, float cb, float cc, float eps, float scale) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ double sums[SM_TPB / 32];
-    __half *A = reinterpret_cast<__half*>(raw), *P = A + SM_SQ, *X = P + SM_SQ;
-    const int ldx = sm_ldx(N), wide = ldx - 8, mn = M * N;
+    extern __shared__ uint8_t raw[];
+    Small m;
+    const int strips = sm_strips(N), mn = M * N;
+    m.begin(raw, strips);
     griddep_wait();
     griddep_launch();
     x += (long long)blockIdx.x * mn;
     out += (long long)blockIdx.x * mn;
     double s = 0.0;
+#pragma unroll 8
     for (int i = threadIdx.x; i < mn; i += SM_TPB) {
         const double v = (double)to_f(x[i]);
         s = fma(v, v, s);
     }
-    const double inv = inverse_norm(block_sum(s, sums), eps) * SX;
-    // zero around the matrix, then the matrix (a tall one transposed)
-    if (M < SM_M || N < wide)
-        for (int i = threadIdx.x; i < SM_M * wide; i += SM_TPB) {
-            const int r = i / wide, c = i % wide;
-            if (r >= M || c >= N) X[r * ldx + c] = X[SM_M * ldx + r * ldx + c] = __float2half_rn(0.f);
-        }
-    for (int i = threadIdx.x; i < mn; i += SM_TPB) {
-        const int r = tall ? i % M : i / N, c = tall ? i / M : i % N;
-        split((float)((double)to_f(x[i]) * inv), X[r * ldx + c], X[SM_M * ldx + r * ldx + c]);
+    const double inv = inverse_norm(block_sum(s, m.bars->sums), eps) * SX;
+    const int row = threadIdx.x & 63;
+    for (int c = (threadIdx.x >> 6) * 8; c < 64 * strips; c += 16) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = row < M && c + e < N ? (float)((double)to_f(x[tall ? (c + e) * M + row : row * N + c + e]) * inv) : 0.f;
+        put_op8(m.X + (c >> 6) * SM_OP, row, c & 63, v);
     }
     const float f = scale / (SX * SP);
-    small_steps(X, ldx, A, P, N, steps, ca, cb, cc, [&](int r, int c, float v, float w) {
-        if (r >= M || c >= N) return;
-        T* o = out + (tall ? c * M + r : r * N + c);
-        o[0] = from_f<T>(v * f);
-        if (c + 1 < N) o[tall ? M : 1] = from_f<T>(w * f);
+    m.steps(strips, steps, ca, cb, cc, [&](int r, int c, const float (&v)[32]) {
+        if (r >= M) return;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (c + e < N) out[tall ? (c + e) * M + r : r * N + c + e] = from_f<T>(v[e] * f);
     });
+    m.end();
 }
 
 // ------------------------------------------------------------------ TTT-Linear, orthogonalised step
@@ -338,77 +368,131 @@ __global__ void __launch_bounds__(256)
 }
 
 // One block per unit, d <= 64: the partials are added in split order, g = (1/N)(G W0 - C) is formed in
-// fp32, orthogonalised (small_steps), and W* = W0 - eta U written.
+// fp32 on the CUDA cores (8 x 4 values a thread), orthogonalised, and W* = W0 - eta U written.
 constexpr int FLD = D + 4;
 constexpr int update_smem_bytes() { return small_smem_bytes(D); }
-__global__ void __launch_bounds__(SM_TPB, 2)
+__global__ void __launch_bounds__(SM_TPB, 3)
     update_kernel(const float* __restrict__ part, const float* __restrict__ w0, float* __restrict__ w_star, int S, int H, int d,
                   float inv_n, float eta, int steps, float ca, float cb, float cc, float eps) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ double sums[SM_TPB / 32];
-    __half *A = reinterpret_cast<__half*>(raw), *P = A + SM_SQ, *X = P + SM_SQ;
-    float *G = reinterpret_cast<float*>(A), *W = reinterpret_cast<float*>(P);  // [k][64 + 4], before the steps
-    static_assert(SM_SQ * 2 >= D * FLD * 4, "G and W0 fit where A and P go");
+    extern __shared__ uint8_t raw[];
+    Small m;
+    m.begin(raw, 1);
+    // G and W0 [k][64 + 4] before the steps, where X, A and the exchange go
+    float *G = reinterpret_cast<float*>(m.X), *W = G + D * FLD;
+    static_assert(2 * D * FLD * 4 <= 2 * SM_OP + SM_EX, "G and W0 fit");
     const long long u = blockIdx.x;
-    const int dd = d * d, tid = threadIdx.x, ldx = sm_ldx(D);
+    const int dd = d * d, tid = threadIdx.x;
     w0 += (u % H) * dd;
-    for (int e = tid; e < DD; e += SM_TPB) {
-        const int r = e / D, c = e % D;
-        W[r * FLD + c] = r < d && c < d ? __ldg(w0 + r * d + c) : 0.f;
+    if (d == D) {
+#pragma unroll
+        for (int i = 0; i < DD / 4 / SM_TPB; ++i) {
+            const int e = (tid + i * SM_TPB) * 4;
+            *reinterpret_cast<float4*>(W + (e / D) * FLD + e % D) = __ldg(reinterpret_cast<const float4*>(w0 + e));
+        }
+    } else {
+        for (int e = tid; e < DD; e += SM_TPB) {
+            const int r = e / D, c = e % D;
+            W[r * FLD + c] = r < d && c < d ? __ldg(w0 + r * d + c) : 0.f;
+        }
     }
     griddep_wait();  // the partials
     griddep_launch();
     part += u * S * 2 * dd;
-    for (int e = tid; e < DD; e += SM_TPB) {  // G is symmetric: rows are its k
-        const int r = e / D, c = e % D;
-        float s = 0.f;
-        if (r < d && c < d)
-            for (int i = 0; i < S; ++i) s += part[(size_t)i * 2 * dd + r * d + c];
-        G[r * FLD + c] = s;
-    }
-    const int tr = (tid >> 4) * 4, tc = (tid & 15) * 4;
-    float acc[4][4];  // -C first: rows tr.., columns tc..
+    const int tr = (tid >> 4) * 8, tc = (tid & 15) * 4;  // rows tr .. + 7, columns tc .. + 3
+    float acc[8][4];  // -C first, from C^T
+    if (d == D) {
+        // G (symmetric: rows are its k) and C^T, a split's loads all in flight
+        float4 g4[8], c4[4][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 8; ++i) g4[i] = make_float4(0.f, 0.f, 0.f, 0.f), c4[i >> 1][i & 1] = g4[i];
+        for (int q = 0; q < S; ++q) {
+            const float4* p4 = reinterpret_cast<const float4*>(part + (size_t)q * 2 * DD);
+            float4 x[8], y[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float s = 0.f;
-            if (tr + i < d && tc + j < d)
-                for (int q = 0; q < S; ++q) s += part[((size_t)q * 2 + 1) * dd + (tc + j) * d + tr + i];
-            acc[i][j] = -s;
+            for (int i = 0; i < 8; ++i) {
+                x[i] = __ldg(p4 + tid + i * SM_TPB);
+                y[i] = __ldg(p4 + (DD + (tc + (i >> 1)) * D + tr) / 4 + (i & 1));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                g4[i].x += x[i].x, g4[i].y += x[i].y, g4[i].z += x[i].z, g4[i].w += x[i].w;
+                float4& c = c4[i >> 1][i & 1];
+                c.x += y[i].x, c.y += y[i].y, c.z += y[i].z, c.w += y[i].w;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = (tid + i * SM_TPB) * 4, j = i >> 1, h = (i & 1) * 4;
+            *reinterpret_cast<float4*>(G + (e / D) * FLD + e % D) = g4[i];
+            const float4 c = c4[j][i & 1];
+            acc[h][j] = -c.x, acc[h + 1][j] = -c.y, acc[h + 2][j] = -c.z, acc[h + 3][j] = -c.w;
+        }
+    } else {
+        for (int e = tid; e < DD; e += SM_TPB) {
+            const int r = e / D, c = e % D;
+            float s = 0.f;
+            if (r < d && c < d)
+                for (int i = 0; i < S; ++i) s += part[(size_t)i * 2 * dd + r * d + c];
+            G[r * FLD + c] = s;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float s = 0.f;
+                if (tr + i < d && tc + j < d)
+                    for (int q = 0; q < S; ++q) s += part[((size_t)q * 2 + 1) * dd + (tc + j) * d + tr + i];
+                acc[i][j] = -s;
+            }
+    }
     __syncthreads();
-    float gw[4][4] = {};
+    float gw[8][4] = {};
 #pragma unroll 4
     for (int k = 0; k < D; ++k) {
-        const float4 a = *reinterpret_cast<const float4*>(G + k * FLD + tr), b = *reinterpret_cast<const float4*>(W + k * FLD + tc);
-        const float ax[4] = {a.x, a.y, a.z, a.w}, bx[4] = {b.x, b.y, b.z, b.w};
+        const float4 a = *reinterpret_cast<const float4*>(G + k * FLD + tr), a2 = *reinterpret_cast<const float4*>(G + k * FLD + tr + 4);
+        const float4 b = *reinterpret_cast<const float4*>(W + k * FLD + tc);
+        const float ax[8] = {a.x, a.y, a.z, a.w, a2.x, a2.y, a2.z, a2.w}, bx[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) gw[i][j] = fmaf(ax[i], bx[j], gw[i][j]);
     }
     double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             acc[i][j] = (acc[i][j] + gw[i][j]) * inv_n;
             s = fma((double)acc[i][j], (double)acc[i][j], s);
         }
-    const double inv = inverse_norm(block_sum(s, sums), eps) * SX;
+    const double inv = inverse_norm(block_sum(s, m.bars->sums), eps) * SX;  // its barrier: G and W0 have been read
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; j += 2)
-            put2(X + (tr + i) * ldx + tc + j, SM_M * ldx, (float)(acc[i][j] * inv), (float)(acc[i][j + 1] * inv));
+    for (int i = 0; i < 8; ++i) {
+        const float v[4] = {(float)(acc[i][0] * inv), (float)(acc[i][1] * inv), (float)(acc[i][2] * inv), (float)(acc[i][3] * inv)};
+        uint2 hi, lo;
+        split4(v, hi, lo);
+        uint8_t* at = m.X + swz<3>((uint32_t)(tr + i) * 128 + (uint32_t)tc * 2);
+        *reinterpret_cast<uint2*>(at) = hi;
+        *reinterpret_cast<uint2*>(at + SM_M * 128) = lo;
+    }
     w_star += u * dd;
-    small_steps(X, ldx, A, P, D, steps, ca, cb, cc, [&](int r, int c, float v, float w) {
-        if (r >= d || c >= d) return;
-        const float f = -eta / (SX * SP);
-        w_star[r * d + c] = fmaf(f, v, __ldg(w0 + r * d + c));
-        if (c + 1 < d) w_star[r * d + c + 1] = fmaf(f, w, __ldg(w0 + r * d + c + 1));
+    const float f = -eta / (SX * SP);
+    m.steps(1, steps, ca, cb, cc, [&](int r, int c, const float (&v)[32]) {
+        if (r >= d) return;
+        if (d == D) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float4 w = __ldg(reinterpret_cast<const float4*>(w0 + r * D + c + e));
+                *reinterpret_cast<float4*>(w_star + r * D + c + e) =
+                    make_float4(fmaf(f, v[e], w.x), fmaf(f, v[e + 1], w.y), fmaf(f, v[e + 2], w.z), fmaf(f, v[e + 3], w.w));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (c + e < d) w_star[r * d + c + e] = fmaf(f, v[e], __ldg(w0 + r * d + c + e));
+        }
     });
+    m.end();
 }
 
 // O = Q W on the CUDA cores for any d <= 128 and type: 64 tokens x 64 output features per block,
