@@ -5,8 +5,8 @@
 // the result touches HBM.  Each operand lies there as 128 rows, 64 of hi and 64 of lo (fp16, as in
 // orth.cuh), and one tcgen05 product of the stacked rows, [hi; lo] [hi | lo], gives hi hi, hi lo and
 // lo hi at once as quarters of a 128 x 128 accumulator: four MMAs of K = 16 for a 64 x 64 x 64 product,
-// 268 cycles.  lo hi sits in the lanes of the other two warps, so each half of the block sends the
-// other half's columns through shared memory and finishes 32 columns of 64 rows.
+// 268 cycles.  lo hi sits in the lanes that the other warps can read, so each side of the block sends the
+// other side's columns through shared memory; a thread finishes 16 columns of a row.
 //
 // The bound is latency: a step is three such products, each waiting for the one before (accumulator
 // out of tensor memory, exchange, rounding to hi + lo, operand written, MMAs).  48 KB of shared memory
@@ -19,7 +19,7 @@ namespace orth {
 
 constexpr int SM_M = 64;                 // rows of a small matrix
 constexpr int SM_N = 256;                // its longer side at most
-constexpr int SM_TPB = 128;
+constexpr int SM_TPB = 256;              // 8 warps, two for each quarter of the accumulator's lanes
 constexpr int SM_OP = 2 * SM_M * 128;    // an operand of 64 columns: 64 rows of hi, 64 of lo, 128-byte swizzle
 constexpr int SM_EX = SM_M * SM_M * 4;   // the exchange
 struct SmallBars {
@@ -43,7 +43,7 @@ __device__ __forceinline__ void put_op8(uint8_t* op, int row, int col, const flo
     *reinterpret_cast<uint4*>(at + SM_M * 128) = make_uint4(l0.x, l0.y, l1.x, l1.y);
 }
 
-// What a block of 128 threads works with
+// What a block works with
 struct Small {
     uint8_t *X, *A;    // strips of X; A, then P
     float* ex;
@@ -79,54 +79,53 @@ struct Small {
         __syncthreads();
         tc::fence_after();
     }
-    // v: columns 32 (warp / 2) .. + 31 of row 32 (warp % 2) + lane of hi hi + hi lo + lo hi
-    __device__ __forceinline__ void take(float (&v)[32]) {
+    // The row and the first of the 16 columns that a thread finishes: warps 0, 1, 4, 5 read the lanes of hi hi
+    // and hi lo and finish columns 0 .. 31, the others read those of lo hi and finish columns 32 .. 63.
+    static __device__ __forceinline__ int row() { return (threadIdx.x >> 5 & 1) * 32 + (threadIdx.x & 31); }
+    static __device__ __forceinline__ int col() { return (threadIdx.x >> 6 & 1) * 32 + (threadIdx.x >> 7) * 16; }
+    // v: the thread's values of hi hi + hi lo + lo hi
+    __device__ __forceinline__ void take(float (&v)[16]) {
         mbar_wait<false>(&bars->done, products++ & 1, TTT_DEVERR_TIMEOUT_TMA);
         tc::fence_after();
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 1) * 32 + lane;
-        const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16);
-        float s[32];
-        if (warp < 2) {
-            float h[32], l[32];
+        const int warp = threadIdx.x >> 5, side = warp >> 1 & 1, c0 = (warp >> 2) * 16;
+        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
+        float s[16];  // for the other side
+        if (side == 0) {
+            float h[16], l[16];
             tc::ld16(at, v);
-            tc::ld16(at + 16, v + 16);
             tc::ld16(at + 32, s);
-            tc::ld16(at + 48, s + 16);
             tc::ld16(at + 64, h);
-            tc::ld16(at + 80, h + 16);
             tc::ld16(at + 96, l);
-            tc::ld16(at + 112, l + 16);
             tc::wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
+            for (int c = 0; c < 16; ++c) {
                 v[c] += h[c];
                 s[c] += l[c];
             }
         } else {
             tc::ld16(at, s);
-            tc::ld16(at + 16, s + 16);
             tc::ld16(at + 32, v);
-            tc::ld16(at + 48, v + 16);
             tc::wait_ld();
         }
-        float* out = ex + (warp < 2 ? 0 : 32 * SM_M) + row;  // [column][row]
-        const float* in = ex + (warp < 2 ? 32 * SM_M : 0) + row;
+        float* out = ex + (side * 32 + c0) * SM_M + row();  // [column][row]
+        const float* in = ex + ((1 - side) * 32 + c0) * SM_M + row();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) out[c * SM_M] = s[c];
+        for (int c = 0; c < 16; ++c) out[c * SM_M] = s[c];
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] += in[c * SM_M];
+        for (int c = 0; c < 16; ++c) v[c] += in[c * SM_M];
     }
 
-    // All steps on X (written, not yet synchronised); the last product goes to last(row, column, v): 32 adjacent
+    // All steps on X (written, not yet synchronised); the last product goes to last(row, column, v): 16 adjacent
     // values of X, times SX SP.
     template <typename Last>
     __device__ __forceinline__ void steps(int strips, int count, float ca, float cb, float cc, Last last) {
-        const int warp = threadIdx.x >> 5, row = (warp & 1) * 32 + (threadIdx.x & 31), col = (warp >> 1) * 32;
+        const int row = this->row(), col = this->col();
         const uint64_t xk = tc::smem_desc(smem_u32(X), 16, 1024, 2), xn = tc::smem_desc(smem_u32(X), SM_M * 128, 1024, 2);
         const uint64_t ak = tc::smem_desc(smem_u32(A), 16, 1024, 2);
+        const float pa = SP * ca, pb = SP / SX * cb, pc = SP / (SX * SX) * cc;  // P = SP (a I + b A + c A^2)
         for (int k = 0; k < count; ++k) {
-            float v[32], a[32];
+            float v[16], a[16];
             written();
             if (threadIdx.x == 0) {
                 for (int s = 0; s < strips; ++s)
@@ -139,9 +138,9 @@ struct Small {
             }
             take(a);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) a[c] *= 1.f / SX;
+            for (int c = 0; c < 16; ++c) a[c] *= 1.f / SX;  // A as it is stored
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) put_op8(A, row, col + c, a + c);
+            for (int c = 0; c < 16; c += 8) put_op8(A, row, col + c, a + c);
             written();
             if (threadIdx.x == 0) {
 #pragma unroll
@@ -150,10 +149,9 @@ struct Small {
             }
             take(v);
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-                v[c] = SP * (fmaf(cc / (SX * SX), v[c], cb / SX * a[c]) + (row == col + c ? ca : 0.f));
+            for (int c = 0; c < 16; ++c) v[c] = fmaf(pc, v[c], pb * a[c]) + (row == col + c ? pa : 0.f);
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) put_op8(A, row, col + c, v + c);
+            for (int c = 0; c < 16; c += 8) put_op8(A, row, col + c, v + c);
             const bool done = k + 1 == count;
             for (int s = 0; s < strips; ++s) {
                 written();
@@ -168,9 +166,9 @@ struct Small {
                     last(row, 64 * s + col, v);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] *= 1.f / SP;
+                    for (int c = 0; c < 16; ++c) v[c] *= 1.f / SP;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8) put_op8(X + s * SM_OP, row, col + c, v + c);
+                    for (int c = 0; c < 16; c += 8) put_op8(X + s * SM_OP, row, col + c, v + c);
                 }
             }
         }
@@ -187,8 +185,9 @@ __device__ __forceinline__ double block_sum(double s, double* sm) {
     return s;
 }
 
-// One block per matrix, X [M][N] with M <= 64, N <= 256.  Thread t holds row t % 64 and every second group
-// of 8 columns; a tall matrix is read along its rows, which are columns of X.
+// One block per matrix, X [M][N] with M <= 64, N <= 256.  Thread t holds row t % 64 and every fourth group
+// of 8 columns (a tall matrix: its rows are the columns of X); up to 64 columns stay in registers between
+// the norm and the first split.
 template <typename T>
 __global__ void __launch_bounds__(SM_TPB, 3)
     small_kernel(const T* x, T* out, int M, int N, int tall, int steps, float ca, float cb, float cc, float eps, float scale) {
@@ -200,27 +199,80 @@ __global__ void __launch_bounds__(SM_TPB, 3)
     griddep_launch();
     x += (long long)blockIdx.x * mn;
     out += (long long)blockIdx.x * mn;
-    double s = 0.0;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < mn; i += SM_TPB) {
-        const double v = (double)to_f(x[i]);
-        s = fma(v, v, s);
-    }
-    const double inv = inverse_norm(block_sum(s, m.bars->sums), eps) * SX;
-    const int row = threadIdx.x & 63;
-    for (int c = (threadIdx.x >> 6) * 8; c < 64 * strips; c += 16) {
-        float v[8];
+    const int row = threadIdx.x & 63, c0 = (threadIdx.x >> 6) * 8;
+    struct alignas(16) Lane {
+        T v[16 / sizeof(T)];
+    };
+    constexpr int VEC = 16 / sizeof(T);
+    const bool wide = !tall && N % VEC == 0 && mn % VEC == 0;  // 16-byte pieces of rows
+    auto load8 = [&](int c, float (&v)[8]) {
+        if (wide) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = row < M && c + e < N ? (float)((double)to_f(x[tall ? (c + e) * M + row : row * N + c + e]) * inv) : 0.f;
+            for (int h = 0; h < 8; h += VEC) {
+                if (row < M && c + h < N) {
+                    const Lane l = *reinterpret_cast<const Lane*>(x + row * N + c + h);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[h + e] = to_f(l.v[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[h + e] = 0.f;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = row < M && c + e < N ? to_f(x[tall ? (c + e) * M + row : row * N + c + e]) : 0.f;
+        }
+    };
+    auto square = [](double s, const float (&v)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fma((double)v[e], (double)v[e], s);
+        return s;
+    };
+    auto put = [&](int c, double inv, float (&v)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (float)((double)v[e] * inv);
         put_op8(m.X + (c >> 6) * SM_OP, row, c & 63, v);
+    };
+    if (strips == 1) {
+        float v[2][8];
+        load8(c0, v[0]);
+        load8(c0 + 32, v[1]);
+        const double s = square(0.0, v[0]) + square(0.0, v[1]);
+        const double inv = inverse_norm(block_sum(s, m.bars->sums), eps) * SX;
+        put(c0, inv, v[0]);
+        put(c0 + 32, inv, v[1]);
+    } else {
+        double s = 0.0;
+        float v[8];
+#pragma unroll 4
+        for (int c = c0; c < 64 * strips; c += 32) {
+            load8(c, v);
+            s = square(s, v);
+        }
+        const double inv = inverse_norm(block_sum(s, m.bars->sums), eps) * SX;
+#pragma unroll 2
+        for (int c = c0; c < 64 * strips; c += 32) {
+            load8(c, v);
+            put(c, inv, v);
+        }
     }
     const float f = scale / (SX * SP);
-    m.steps(strips, steps, ca, cb, cc, [&](int r, int c, const float (&v)[32]) {
+    m.steps(strips, steps, ca, cb, cc, [&](int r, int c, const float (&v)[16]) {
         if (r >= M) return;
+        if (wide) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (c + e < N) out[tall ? (c + e) * M + r : r * N + c + e] = from_f<T>(v[e] * f);
+            for (int h = 0; h < 16; h += VEC)
+                if (c + h < N) {
+                    Lane l;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) l.v[e] = from_f<T>(v[h + e] * f);
+                    *reinterpret_cast<Lane*>(out + r * N + c + h) = l;
+                }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (c + e < N) out[tall ? (c + e) * M + r : r * N + c + e] = from_f<T>(v[e] * f);
+        }
     });
     m.end();
 }
@@ -368,7 +420,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // One block per unit, d <= 64: the partials are added in split order, g = (1/N)(G W0 - C) is formed in
-// fp32 on the CUDA cores (8 x 4 values a thread), orthogonalised, and W* = W0 - eta U written.
+// fp32 on the CUDA cores (4 x 4 values a thread), orthogonalised, and W* = W0 - eta U written.
 constexpr int FLD = D + 4;
 constexpr int update_smem_bytes() { return small_smem_bytes(D); }
 __global__ void __launch_bounds__(SM_TPB, 3)
@@ -398,34 +450,33 @@ __global__ void __launch_bounds__(SM_TPB, 3)
     griddep_wait();  // the partials
     griddep_launch();
     part += u * S * 2 * dd;
-    const int tr = (tid >> 4) * 8, tc = (tid & 15) * 4;  // rows tr .. + 7, columns tc .. + 3
-    float acc[8][4];  // -C first, from C^T
+    const int tr = (tid >> 4) * 4, tc = (tid & 15) * 4;  // rows tr .. + 3, columns tc .. + 3
+    float acc[4][4];  // -C first, from C^T
     if (d == D) {
         // G (symmetric: rows are its k) and C^T, a split's loads all in flight
-        float4 g4[8], c4[4][2];
+        float4 g4[4], c4[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g4[i] = make_float4(0.f, 0.f, 0.f, 0.f), c4[i >> 1][i & 1] = g4[i];
+        for (int i = 0; i < 4; ++i) g4[i] = c4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
         for (int q = 0; q < S; ++q) {
             const float4* p4 = reinterpret_cast<const float4*>(part + (size_t)q * 2 * DD);
-            float4 x[8], y[8];
+            float4 x[4], y[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 x[i] = __ldg(p4 + tid + i * SM_TPB);
-                y[i] = __ldg(p4 + (DD + (tc + (i >> 1)) * D + tr) / 4 + (i & 1));
+                y[i] = __ldg(p4 + (DD + (tc + i) * D + tr) / 4);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 g4[i].x += x[i].x, g4[i].y += x[i].y, g4[i].z += x[i].z, g4[i].w += x[i].w;
-                float4& c = c4[i >> 1][i & 1];
-                c.x += y[i].x, c.y += y[i].y, c.z += y[i].z, c.w += y[i].w;
+                c4[i].x += y[i].x, c4[i].y += y[i].y, c4[i].z += y[i].z, c4[i].w += y[i].w;
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = (tid + i * SM_TPB) * 4, j = i >> 1, h = (i & 1) * 4;
+        for (int i = 0; i < 4; ++i) {
+            const int e = (tid + i * SM_TPB) * 4;
             *reinterpret_cast<float4*>(G + (e / D) * FLD + e % D) = g4[i];
-            const float4 c = c4[j][i & 1];
-            acc[h][j] = -c.x, acc[h + 1][j] = -c.y, acc[h + 2][j] = -c.z, acc[h + 3][j] = -c.w;
+            acc[0][i] = -c4[i].x, acc[1][i] = -c4[i].y, acc[2][i] = -c4[i].z, acc[3][i] = -c4[i].w;
         }
     } else {
         for (int e = tid; e < DD; e += SM_TPB) {
@@ -438,7 +489,7 @@ __global__ void __launch_bounds__(SM_TPB, 3)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 float s = 0.f;
                 if (tr + i < d && tc + j < d)
                     for (int q = 0; q < S; ++q) s += part[((size_t)q * 2 + 1) * dd + (tc + j) * d + tr + i];
@@ -446,20 +497,19 @@ __global__ void __launch_bounds__(SM_TPB, 3)
             }
     }
     __syncthreads();
-    float gw[8][4] = {};
-#pragma unroll 4
+    float gw[4][4] = {};
+#pragma unroll 8
     for (int k = 0; k < D; ++k) {
-        const float4 a = *reinterpret_cast<const float4*>(G + k * FLD + tr), a2 = *reinterpret_cast<const float4*>(G + k * FLD + tr + 4);
-        const float4 b = *reinterpret_cast<const float4*>(W + k * FLD + tc);
-        const float ax[8] = {a.x, a.y, a.z, a.w, a2.x, a2.y, a2.z, a2.w}, bx[4] = {b.x, b.y, b.z, b.w};
+        const float4 a = *reinterpret_cast<const float4*>(G + k * FLD + tr), b = *reinterpret_cast<const float4*>(W + k * FLD + tc);
+        const float ax[4] = {a.x, a.y, a.z, a.w}, bx[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) gw[i][j] = fmaf(ax[i], bx[j], gw[i][j]);
     }
     double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             acc[i][j] = (acc[i][j] + gw[i][j]) * inv_n;
@@ -467,7 +517,7 @@ __global__ void __launch_bounds__(SM_TPB, 3)
         }
     const double inv = inverse_norm(block_sum(s, m.bars->sums), eps) * SX;  // its barrier: G and W0 have been read
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float v[4] = {(float)(acc[i][0] * inv), (float)(acc[i][1] * inv), (float)(acc[i][2] * inv), (float)(acc[i][3] * inv)};
         uint2 hi, lo;
         split4(v, hi, lo);
@@ -477,18 +527,18 @@ __global__ void __launch_bounds__(SM_TPB, 3)
     }
     w_star += u * dd;
     const float f = -eta / (SX * SP);
-    m.steps(1, steps, ca, cb, cc, [&](int r, int c, const float (&v)[32]) {
+    m.steps(1, steps, ca, cb, cc, [&](int r, int c, const float (&v)[16]) {
         if (r >= d) return;
         if (d == D) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < 16; e += 4) {
                 const float4 w = __ldg(reinterpret_cast<const float4*>(w0 + r * D + c + e));
                 *reinterpret_cast<float4*>(w_star + r * D + c + e) =
                     make_float4(fmaf(f, v[e], w.x), fmaf(f, v[e + 1], w.y), fmaf(f, v[e + 2], w.z), fmaf(f, v[e + 3], w.w));
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
                 if (c + e < d) w_star[r * d + c + e] = fmaf(f, v[e], __ldg(w0 + r * d + c + e));
         }
     });
