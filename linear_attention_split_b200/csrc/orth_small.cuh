@@ -9,8 +9,10 @@
 // other side's columns through shared memory; a thread finishes 16 columns of a row.
 //
 // The bound is latency: a step is three such products, each waiting for the one before (accumulator
-// out of tensor memory, exchange, rounding to hi + lo, operand written, MMAs).  48 KB of shared memory
-// and 128 columns of tensor memory let four blocks share an SM and fill one another's gaps.
+// out of tensor memory, exchange, rounding to hi + lo, operand written, MMAs; about 1400 cycles).  Several
+// blocks share an SM and fill one another's gaps.  Compiled for two blocks an SM nothing spills (32 units of
+// the TTT-Linear step: 27 us against 30 for three blocks); with more matrices than two blocks an SM hold, three
+// make one wave of up to 444 (384 units: 41 us against 51).
 #pragma once
 #include "common.cuh"
 #include "orth.cuh"
@@ -188,8 +190,8 @@ __device__ __forceinline__ double block_sum(double s, double* sm) {
 // One block per matrix, X [M][N] with M <= 64, N <= 256.  Thread t holds row t % 64 and every fourth group
 // of 8 columns (a tall matrix: its rows are the columns of X); up to 64 columns stay in registers between
 // the norm and the first split.
-template <typename T>
-__global__ void __launch_bounds__(SM_TPB, 3)
+template <typename T, int PER_SM>
+__global__ void __launch_bounds__(SM_TPB, PER_SM)
     small_kernel(const T* x, T* out, int M, int N, int tall, int steps, float ca, float cb, float cc, float eps, float scale) {
     extern __shared__ uint8_t raw[];
     Small m;
@@ -423,7 +425,8 @@ __global__ void __launch_bounds__(256)
 // fp32 on the CUDA cores (4 x 4 values a thread), orthogonalised, and W* = W0 - eta U written.
 constexpr int FLD = D + 4;
 constexpr int update_smem_bytes() { return small_smem_bytes(D); }
-__global__ void __launch_bounds__(SM_TPB, 3)
+template <int PER_SM>
+__global__ void __launch_bounds__(SM_TPB, PER_SM)
     update_kernel(const float* __restrict__ part, const float* __restrict__ w0, float* __restrict__ w_star, int S, int H, int d,
                   float inv_n, float eta, int steps, float ca, float cb, float cc, float eps) {
     extern __shared__ uint8_t raw[];

@@ -971,11 +971,13 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
     if (p.small) {
         const int smem = orth::small_smem_bytes(p.N);
         if (orth::small_smem_bytes(orth::SM_N) > dev->smem_optin) return TTT_ERR_UNSUPPORTED;
-        static SmemRecord record;
-        if (!allow_smem(orth::small_kernel<T>, orth::small_smem_bytes(orth::SM_N), record)) return TTT_ERR_CUDA;
-        if (int rc = launch_pdl(orth::small_kernel<T>, dim3((unsigned)U), orth::SM_TPB, smem, st, x, out, p.M, p.N, p.tall,
-                                steps, a, b, c, eps, scale))
-            return rc;
+        auto run = [&](auto per_sm) -> int {
+            const auto kern = orth::small_kernel<T, per_sm()>;
+            static SmemRecord record;
+            if (!allow_smem(kern, orth::small_smem_bytes(orth::SM_N), record)) return TTT_ERR_CUDA;
+            return launch_pdl(kern, dim3((unsigned)U), orth::SM_TPB, smem, st, x, out, p.M, p.N, p.tall, steps, a, b, c, eps, scale);
+        };
+        if (int rc = U <= 2LL * dev->sms ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 3>())) return rc;
         return launched(1);
     }
     if (orth_tiles(false, p.M, p.N, 64) > 65535) return TTT_ERR_UNSUPPORTED;
@@ -1151,11 +1153,14 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
     }
     if (d <= orth::SM_M) {
         const int smem = orth::update_smem_bytes();
-        static SmemRecord record;
-        if (!allow_smem(orth::update_kernel, smem, record)) return TTT_ERR_CUDA;
-        if (int rc = launch_pdl(orth::update_kernel, dim3((unsigned)U), orth::SM_TPB, smem, st, (const float*)part, w0, w, p.S, H, d,
-                                inv_n, eta, steps, a, b, c, eps))
-            return rc;
+        auto run = [&](auto per_sm) -> int {
+            const auto kern = orth::update_kernel<per_sm()>;
+            static SmemRecord record;
+            if (!allow_smem(kern, smem, record)) return TTT_ERR_CUDA;
+            return launch_pdl(kern, dim3((unsigned)U), orth::SM_TPB, smem, st, (const float*)part, w0, w, p.S, H, d, inv_n, eta, steps,
+                              a, b, c, eps);
+        };
+        if (int rc = U <= 2LL * dev->sms ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 3>())) return rc;
         launched(2);
     } else {
         float* g = reinterpret_cast<float*>(ws + p.g);
