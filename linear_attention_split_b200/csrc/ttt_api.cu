@@ -929,7 +929,8 @@ int orth_check(int steps, float a, float b, float c, float eps) {
 }
 // A product's tile width and split of K over a cluster, the fastest by count: K blocks at their cycles
 // (Config::BLOCK), a tile's start and end about 3000 and 35 a column (7 more accumulators: as much again),
-// the exchange of a split tile about 2000 and 20 a column, and 148 SMs holding 148, 72, 33 or 15 clusters of
+// the exchange of a split tile about 2000 and 20 a column (500 and 10 while half of the SMs are idle: 384 x
+// 384 times itself in two halves 97 us for all steps of 384 x 1536, unsplit 101), and 148 SMs holding 148, 72, 33 or 15 clusters of
 // 1, 2, 4 or 8.  Full precision takes no more than 50 MMAs into one accumulator where it can.
 struct OrthPick {
     int bn = 0, S = 0;
@@ -948,7 +949,8 @@ void orth_consider(OrthPick& best, int tiles, long long U, int kblocks) {
     for (int i = 0, S = 1; i < (C::EXCHANGE ? 4 : 1); ++i, S *= 2) {
         if (S > 1 && kblocks < 2 * S) break;
         const long long per = (kblocks + S - 1) / S, waves = (tiles * U + room[i] - 1) / room[i];
-        long long cycles = waves * (per * C::BLOCK + 3000 + 35 * C::BN + (S > 1 ? 2000 + 20 * C::BN : 0));
+        const long long exchange = tiles * U * S <= 74 ? 500 + 10 * C::BN : 2000 + 20 * C::BN;
+        long long cycles = waves * (per * C::BLOCK + 3000 + 35 * C::BN + (S > 1 ? exchange : 0));
         if (C::FL && per * 4 > 50 * C::ACC) cycles *= 2;
         if (!best.bn || cycles < best.cycles) {
             best.bn = C::BN;

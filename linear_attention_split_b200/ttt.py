@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import re
 
@@ -353,15 +354,50 @@ def ttt_linear_chunked_bidir_noalloc(q, k, v, w0, out, chunk, eta=1.0, stream=No
 NS_COEF = (3.4445, -4.7750, 2.0315)  # the usual quintic of the Newton-Schulz steps
 
 
-def _one_device(first, *more):
-    """The index of the tensors' device, which has to be one CUDA device."""
-    dev = first.get_device()
-    for t in more:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be on one device")
+# The checks of arguments below go by what a check can depend on: each tensor's type, shape, strides and
+# device.  A function that has passed them once for such a description keeps what it found (functools.lru_cache;
+# nothing is kept by a tensor's identity or address, and a refusal is not kept), which is most of a call's host time.
+def _sig(t):
+    return None if t is None else (t.dtype, t.shape, t.stride(), t.get_device())
+
+
+def _sig_dense(sig):
+    want = 1
+    for n, st in zip(reversed(sig[1]), reversed(sig[2])):
+        if n != 1 and st != want:
+            return 0 in sig[1]
+        want *= n
+    return True
+
+
+def _sig_device(*sigs):
+    """The index of the device, which has to be one CUDA device."""
+    dev = sigs[0][3]
+    if any(s is not None and s[3] != dev for s in sigs):
+        raise ValueError("tensors must be on one device")
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
     return dev
+
+
+def _sig_type(*sigs):
+    """The library's type of dense tensors of one dtype and shape."""
+    dtype, shape = sigs[0][:2]
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    for s in sigs:
+        if s[0] is not dtype:
+            raise TypeError("tensors must share one dtype")
+        if s[1] != shape:
+            raise ValueError("tensors must have one shape")
+        if not _sig_dense(s):
+            raise ValueError("tensors must be contiguous CUDA tensors")
+    return _DT[dtype]
+
+
+def _sig_vector(sig, C, name):
+    if sig is not None and (sig[0] is not torch.float32 or tuple(sig[1]) != (C,) or not _sig_dense(sig)):
+        raise ValueError(f"{name} must be a contiguous fp32 tensor [C]")
 
 
 @functools.lru_cache(maxsize=512)
@@ -410,43 +446,34 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows(x):
-    """(rows, C) of a tensor [..., C]."""
-    C = x.shape[-1] if x.dim() else 0
-    return (x.numel() // C if C else 0), C
+@functools.lru_cache(maxsize=512)
+def _norm_args(x, gamma, beta, *like_x):
+    """(rows, C, type, device) of a layer norm of x [..., C] with vectors gamma, beta [C]."""
+    dt = _sig_type(x, *like_x)
+    shape = x[1]
+    C = shape[-1] if len(shape) else 0
+    _sig_vector(gamma, C, "gamma")
+    _sig_vector(beta, C, "beta")
+    return (math.prod(shape[:-1]) if C else 0), C, dt, _sig_device(x, gamma, beta, *like_x)
 
 
-def _vector(t, C, name):
-    if t is not None and (t.dtype is not torch.float32 or t.dim() != 1 or t.shape[0] != C or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous fp32 tensor [C]")
+def _layernorm(x, gamma, beta, y, eps, stream, args):
+    rows, C, dt, dev = args
+    _call(lib().ttt_layernorm, dev, stream, x.data_ptr(), gamma.data_ptr(), _at(beta), y.data_ptr(), rows, C, eps, dt)
+    return y
 
 
-def _dense(first, *more):
-    """The library's type of dense tensors of one dtype and shape."""
-    dtype, shape = first.dtype, first.shape
-    if dtype not in _DT:
-        raise TypeError(f"unsupported dtype {dtype}")
-    if not first.is_contiguous():
-        raise ValueError("tensors must be contiguous CUDA tensors")
-    for t in more:
-        if t.dtype is not dtype:
-            raise TypeError("tensors must share one dtype")
-        if t.shape != shape:
-            raise ValueError("tensors must have one shape")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous CUDA tensors")
-    return _DT[dtype]
+def _layernorm_bwd(dy, x, gamma, dx, dgamma, dbeta, eps, workspace, stream, args):
+    rows, C, dt, dev = args
+    ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_layernorm_bwd_workspace_bytes", dev, rows, C, dt), workspace, dev, stream)
+    _call(lib().ttt_layernorm_bwd, dev, stream, dy.data_ptr(), x.data_ptr(), gamma.data_ptr(), dx.data_ptr(), dgamma.data_ptr(),
+          _at(dbeta), rows, C, eps, dt, ws, nbytes)
+    return dx, dgamma, dbeta
 
 
 def ttt_layernorm(x, gamma, beta, y, eps=1e-6, stream=None):
     """Layer norm over the last axis: x, y [..., C] (y may be x); gamma, beta [C] fp32, beta may be None."""
-    dt = _dense(x, y)
-    rows, C = _rows(x)
-    _vector(gamma, C, "gamma")
-    _vector(beta, C, "beta")
-    dev = _one_device(x, gamma, beta, y)
-    _call(lib().ttt_layernorm, dev, stream, _at(x), _at(gamma), _at(beta), _at(y), rows, C, eps, dt)
-    return y
+    return _layernorm(x, gamma, beta, y, eps, stream, _norm_args(_sig(x), _sig(gamma), _sig(beta), _sig(y)))
 
 
 def ttt_layernorm_bwd_workspace_bytes(rows, C, dtype):
@@ -455,28 +482,52 @@ def ttt_layernorm_bwd_workspace_bytes(rows, C, dtype):
 
 def ttt_layernorm_bwd(dy, x, gamma, dx, dgamma, dbeta=None, eps=1e-6, workspace=None, stream=None):
     """Gradients of ttt_layernorm: dx [..., C] (may be dy or x), dgamma and dbeta [C] fp32 (dbeta may be None)."""
-    dt = _dense(x, dy, dx)
-    rows, C = _rows(x)
-    for t, name in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")):
-        _vector(t, C, name)
-    dev = _one_device(x, dy, gamma, dx, dgamma, dbeta)
-    ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_layernorm_bwd_workspace_bytes", dev, rows, C, dt), workspace, dev, stream)
-    _call(lib().ttt_layernorm_bwd, dev, stream, _at(dy), _at(x), _at(gamma), _at(dx), _at(dgamma), _at(dbeta),
-          rows, C, eps, dt, ws, nbytes)
-    return dx, dgamma, dbeta
+    args = _norm_args(_sig(x), _sig(gamma), _sig(dgamma), _sig(dy), _sig(dx))
+    _norm_args(_sig(x), _sig(gamma), _sig(dbeta))
+    return _layernorm_bwd(dy, x, gamma, dx, dgamma, dbeta, eps, workspace, stream, args)
 
 
-@functools.lru_cache(maxsize=256)
-def _ints(*values):
-    """A host array of int that the library reads (kept by its values)."""
-    return (ctypes.c_int * max(len(values), 1))(*values)
+@functools.lru_cache(maxsize=512)
+def _rope_args(q, k, q_out, k_out, pos, dims, grid):
+    """The library's arguments behind the tensors' pointers; an output without a description is dense."""
+    if (grid is None) == (pos is None):
+        raise ValueError("give either grid or pos")
+    dtype, shape = q[:2]
+    if len(shape) != 4:
+        raise ValueError("q, k and their outputs must be [B, H, N, d]")
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    B, H, N, d = shape
+    strides = []
+    for t in (q, k, q_out, k_out):
+        if t is None:
+            strides += [H * N * d, N * d, d]
+            continue
+        if t[0] is not dtype:
+            raise TypeError("q, k and their outputs must share one dtype")
+        if t[1] != shape:
+            raise ValueError("q, k and their outputs must have one shape")
+        if t[2][3] != 1 and d != 1:
+            raise ValueError("the features of a head must be adjacent")
+        strides += t[2][:3]
+    dev = _sig_device(q, k, q_out, k_out, pos)
+    axes = len(dims)
+    if grid is not None and len(grid) != axes:
+        raise ValueError("grid and dims must have one length")
+    batched = 0
+    if pos is not None:
+        batched = int(len(pos[1]) == 3)
+        if pos[0] is not torch.float32 or not _sig_dense(pos) or tuple(pos[1]) != ((B, N, axes) if batched else (N, axes)):
+            raise ValueError("pos must be contiguous fp32 [N, axes] or [B, N, axes]")
+    ints = ctypes.c_int * max(axes, 1)
+    return (batched, None if grid is None else ints(*grid), ints(*dims), axes, B, H, N, d), (ctypes.c_longlong * 12)(*strides), \
+        _DT[dtype], dev
 
 
-@functools.lru_cache(maxsize=256)
-def _strides(*tensors):
-    """The host array of (b, h, n) strides of the tensors, from their stride tuples; a missing one is zeros."""
-    flat = [v for t in tensors for v in (t[:3] if t else (0, 0, 0))]
-    return (ctypes.c_longlong * len(flat))(*flat)
+def _rope(q, k, q_out, k_out, pos, base, interleaved, inverse, stream, args):
+    sizes, strides, dt, dev = args
+    _call(lib().ttt_rope, dev, stream, q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), _at(pos), *sizes, base, interleaved,
+          inverse, strides, dt)
 
 
 def ttt_rope(q, k, q_out, k_out, dims, grid=None, pos=None, base=10000.0, interleaved=False, inverse=False, stream=None):
@@ -485,39 +536,8 @@ def ttt_rope(q, k, q_out, k_out, dims, grid=None, pos=None, base=10000.0, interl
     the token grid, or pos, fp32 [N, axes] or [B, N, axes].  inverse: turn back, which is the backward pass."""
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    if (grid is None) == (pos is None):
-        raise ValueError("give either grid or pos")
-    shape, dtype = q.shape, q.dtype
-    if len(shape) != 4:
-        raise ValueError("q, k and their outputs must be [B, H, N, d]")
-    if dtype not in _DT:
-        raise TypeError(f"unsupported dtype {dtype}")
-    B, H, N, d = shape
-    st = []
-    for t in (q, k, q_out, k_out):
-        if t is None:
-            st.append(None)
-            continue
-        if t.dtype != dtype:
-            raise TypeError("q, k and their outputs must share one dtype")
-        if t.shape != shape:
-            raise ValueError("q, k and their outputs must have one shape")
-        st.append(t.stride())
-        if st[-1][3] != 1 and d != 1:
-            raise ValueError("the features of a head must be adjacent")
-    dev = _one_device(q, k, q_out, k_out, pos)
-    axes = len(dims)
-    if grid is not None and len(grid) != axes:
-        raise ValueError("grid and dims must have one length")
-    batched = 0
-    if pos is not None:
-        batched = int(pos.dim() == 3)
-        if pos.dtype != torch.float32 or not pos.is_contiguous() or \
-                tuple(pos.shape) != ((B, N, axes) if batched else (N, axes)):
-            raise ValueError("pos must be contiguous fp32 [N, axes] or [B, N, axes]")
-    _call(lib().ttt_rope, dev, stream, q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), _at(pos), batched,
-          _ints(*grid) if grid is not None else None, _ints(*dims), axes, B, H, N, d, base, interleaved, inverse,
-          _strides(*st), _DT[dtype])
+    args = _rope_args(_sig(q), _sig(k), _sig(q_out), _sig(k_out), _sig(pos), tuple(dims), None if grid is None else tuple(grid))
+    _rope(q, k, q_out, k_out, pos, base, interleaved, inverse, stream, args)
     return q_out, k_out
 
 
@@ -527,16 +547,24 @@ def ttt_orthogonalize_workspace_bytes(U, m, n, dtype):
 
 def ttt_orthogonalize(x, out, steps=5, coef=NS_COEF, eps=1e-7, scale=1.0, workspace=None, stream=None):
     """out = scale * the Newton-Schulz steps of each matrix of x [..., m, n] (out may be x)."""
-    dt = _dense(x, out)
-    if x.dim() < 2:
+    return _orthogonalize(x, out, steps, coef, eps, scale, workspace, stream, _orth_args(_sig(x), _sig(out)))
+
+
+@functools.lru_cache(maxsize=512)
+def _orth_args(x, *like_x):
+    """(U, m, n, type, device) of matrices [..., m, n]."""
+    dt = _sig_type(x, *like_x)
+    if len(x[1]) < 2:
         raise ValueError("x must be [..., m, n]")
-    dev = _one_device(x, out)
-    m, n = x.shape[-2:]
-    U = x.numel() // (m * n) if m * n else 0
+    m, n = x[1][-2:]
+    return math.prod(x[1][:-2]), m, n, dt, _sig_device(x, *like_x)
+
+
+def _orthogonalize(x, out, steps, coef, eps, scale, workspace, stream, args):
+    U, m, n, dt, dev = args
     a, b, c = coef
     ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_orthogonalize_workspace_bytes", dev, U, m, n, dt), workspace, dev, stream)
-    _call(lib().ttt_orthogonalize, dev, stream, _at(x), _at(out), U, m, n, steps, a, b, c, eps, scale, dt, ws,
-          nbytes)
+    _call(lib().ttt_orthogonalize, dev, stream, x.data_ptr(), out.data_ptr(), U, m, n, steps, a, b, c, eps, scale, dt, ws, nbytes)
     return out
 
 
@@ -547,19 +575,25 @@ def ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dtype):
 def ttt_linear_fullbatch_orth(q, k, v, w0, out, w_star=None, eta=0.1, steps=5, coef=NS_COEF, eps=1e-7, workspace=None,
                               stream=None):
     """TTT-Linear whose inner step goes along the orthogonalised gradient; tensors as for ttt_linear_fullbatch."""
-    dt = _dense(q, k, v, out)
-    _weights(w0, w_star)
-    if q.dim() != 4:
-        raise ValueError("q, k, v and out must be [B, H, N, d]")
-    B, H, N, d = q.shape
-    if tuple(w0.shape) != (H, d, d) or (w_star is not None and tuple(w_star.shape) != (B, H, d, d)):
-        raise ValueError("w0 must be [H, d, d] and w_star [B, H, d, d]")
-    dev = _one_device(q, k, v, w0, out, w_star)
+    B, H, N, d, dt, dev = _linear_orth_args(_sig(q), _sig(k), _sig(v), _sig(out), _sig(w0), _sig(w_star))
     a, b, c = coef
-    ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_linear_fullbatch_orth_workspace_bytes", dev, B, H, N, d, dt), workspace, dev, stream)
-    _call(lib().ttt_linear_fullbatch_orth, dev, stream, _at(q), _at(k), _at(v), _at(w0), _at(out), _at(w_star),
-          B, H, N, d, eta, steps, a, b, c, eps, dt, ws, nbytes)
+    ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_linear_fullbatch_orth_workspace_bytes", dev, B, H, N, d, dt), workspace, dev,
+                                 stream)
+    _call(lib().ttt_linear_fullbatch_orth, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), w0.data_ptr(), out.data_ptr(),
+          _at(w_star), B, H, N, d, eta, steps, a, b, c, eps, dt, ws, nbytes)
     return out
+
+
+@functools.lru_cache(maxsize=512)
+def _linear_orth_args(q, k, v, out, w0, w_star):
+    dt = _sig_type(q, k, v, out)
+    if len(q[1]) != 4:
+        raise ValueError("q, k, v and out must be [B, H, N, d]")
+    B, H, N, d = q[1]
+    for w, shape in ((w0, (H, d, d)), (w_star, (B, H, d, d))):
+        if w is not None and (w[0] is not torch.float32 or tuple(w[1]) != shape or not _sig_dense(w)):
+            raise ValueError("w0 must be [H, d, d] and w_star [B, H, d, d], contiguous fp32")
+    return B, H, N, d, dt, _sig_device(q, k, v, out, w0, w_star)
 
 
 TTT_FAULT_SKIP_LOAD = 0x1
@@ -648,20 +682,23 @@ def linear_chunked_bidir(q, k, v, w0, chunk, eta=1.0):
 
 
 def layernorm(x, gamma, beta=None, eps=1e-6):
-    return ttt_layernorm(x, gamma, beta, torch.empty_like(x), eps)
+    args = _norm_args(_sig(x), _sig(gamma), _sig(beta))
+    return _layernorm(x, gamma, beta, torch.empty_like(x), eps, None, args)
 
 
 def layernorm_bwd(dy, x, gamma, eps=1e-6, with_dbeta=True):
     """(dx, dgamma, dbeta); dbeta is None without with_dbeta."""
-    return ttt_layernorm_bwd(dy, x, gamma, torch.empty_like(x), torch.empty_like(gamma),
-                             torch.empty_like(gamma) if with_dbeta else None, eps)
+    args = _norm_args(_sig(x), _sig(gamma), None, _sig(dy))
+    return _layernorm_bwd(dy, x, gamma, torch.empty_like(x), torch.empty_like(gamma),
+                          torch.empty_like(gamma) if with_dbeta else None, eps, None, None, args)
 
 
 def rope(q, k=None, dims=None, grid=None, pos=None, base=10000.0, interleaved=False, inverse=False):
     """q and k turned to their positions, each contiguous [B, H, N, d]; without k, q alone."""
+    args = _rope_args(_sig(q), _sig(k), None, None, _sig(pos), tuple(dims), None if grid is None else tuple(grid))
     q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
-    ttt_rope(q, k, q_out, k_out, dims, grid, pos, base, interleaved, inverse)
+    _rope(q, k, q_out, k_out, pos, base, interleaved, inverse, None, args)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -671,7 +708,7 @@ def rope_bwd(dq, dk=None, dims=None, grid=None, pos=None, base=10000.0, interlea
 
 
 def orthogonalize(x, steps=5, coef=NS_COEF, eps=1e-7, scale=1.0):
-    return ttt_orthogonalize(x, torch.empty_like(x), steps, coef, eps, scale)
+    return _orthogonalize(x, torch.empty_like(x), steps, coef, eps, scale, None, None, _orth_args(_sig(x)))
 
 
 def linear_fullbatch_orth(q, k, v, w0, eta=0.1, steps=5, coef=NS_COEF, eps=1e-7, with_w_star=False):
