@@ -189,9 +189,8 @@ struct Config {
     static constexpr int STAGE = (1 + FL) * OPB + (1 + SL) * SECOND;
     static constexpr bool CROSS = FL || SL;
     static constexpr int ACCS = ACC + CROSS;
-    static constexpr int ISSUERS = CROSS ? 1 : 2;
-    static constexpr int FRONT = 32 * (1 + ISSUERS), THREADS = FRONT + 256;  // producer, issuers; eight epilogue warps
-    static_assert(CROSS || ACC == ISSUERS, "hi hi alone: one accumulator for each issuer");
+    static constexpr int FRONT = 96, THREADS = FRONT + 256;  // producer and two issuers; eight epilogue warps
+    static_assert(CROSS || (ACC == 2 && STAGES % 2 == 0), "hi hi alone: an accumulator and slots of its own for each issuer");
     static constexpr int COLS = ACCS * BN;                         // of tensor memory
     static constexpr int EXCHANGE = BN > 128 ? 0 : TM * BN * 4;    // the S partial slices of a tile
     // the ring; over it the exchange and what is staged
@@ -372,9 +371,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_con
         tma_prefetch_desc(KIND <= POLY ? &maps.second_k : &maps.second_mn);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->empty[s], C::CROSS ? 2 : 1);
         }
-        mbar_init(&bars->done, C::ISSUERS);
+        mbar_init(&bars->done, 2);
         mbar_fence_init();
     }
     if (warp == 1) tc::alloc(&bars->tmem_base, C::COLS);
@@ -385,20 +384,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_con
     griddep_launch();
     const uint32_t tmem = bars->tmem_base;
 
-    // The MMAs of one issuing thread.  One thread spends about 300 cycles a K block on its barriers (a test of a
-    // phase that is over already takes 200) while the tensor cores wait.  The four MMAs of hi hi alone are too
-    // short to cover that: two issuers take alternate K blocks there, each with an accumulator of its own, so
-    // that nothing depends on how they interleave (1024 x 4096 bf16 180 -> 165 us).  Twelve MMAs are faster from
-    // one thread (384 x 1536 fp32 101 us; hi hi and cross terms from two threads 110).  The issuer's number is a
-    // constant: addresses that come from the thread's index cost a move to the uniform registers for each MMA.
+    // The MMAs of one issuing thread.  A thread spends about 300 cycles a K block on its barriers (a test of a
+    // phase that is over already takes 200) while the tensor cores wait, so there are two: with cross terms the
+    // first issues hi hi and the second the rest, hi hi alone they take alternate K blocks.  Either way each has
+    // accumulators of its own, so nothing depends on how the two interleave (one issuer against two: 1024 x 1024
+    // fp32 155 against 138 us, 1024 x 4096 bf16 180 against 163).  The issuer's number is a constant: addresses
+    // that come from the thread's index cost a move to the uniform registers for each MMA (384 x 1536 fp32 113 us
+    // that way, 97 so).
     auto issue = [&](auto issuer) {
         constexpr int j = decltype(issuer)::value;
-        int acc = j, count = 0;  // the hi hi accumulator in use, and its MMAs so far
+        int acc = C::CROSS ? 0 : j, count = 0;  // the hi hi accumulator in use, and its MMAs so far
         bool ready = false;
-        for (int i = j; i < nk; i += C::ISSUERS) {
+        constexpr int FROM = C::CROSS ? 0 : j, STEP = C::CROSS ? 1 : 2;
+        for (int i = FROM; i < nk; i += STEP) {
             const int slot = i % C::STAGES, t = (k0 + i) * KB / TM;
             if (!ready) mbar_wait(&bars->full[slot], (i / C::STAGES) & 1, TTT_DEVERR_TIMEOUT_TMA);
-            const int n = i + C::ISSUERS;  // the next block's phase is asked for ahead of this block's MMAs
+            const int n = i + STEP;  // the next block's phase is asked for ahead of this block's MMAs
             ready = n < nk && mbar_test_wait(&bars->full[n % C::STAGES], (n / C::STAGES) & 1);
             tc::fence_after();
             const int fm = KIND != GRAM && t < bi, sm = KIND >= NEXT || (KIND == POLY && t < j0 / TM);  // MN-major
@@ -410,13 +411,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_con
 #pragma unroll
             for (int ks = 0; ks < KB / 16; ++ks) {
                 const uint64_t f = fh + fstep * ks, s = sh + sstep * ks;
-                if (C::CROSS && count == len) {
-                    ++acc;
-                    count = 0;
+                if (!C::CROSS || j == 0) {
+                    if (C::CROSS && count == len) {
+                        ++acc;
+                        count = 0;
+                    }
+                    tc::mma_bf16(tmem + acc * C::BN, f, s, idesc, count++ > 0);
+                } else {
+                    if (C::SL) tc::mma_bf16(cross, f, s + (C::SECOND >> 4), idesc, i > 0 || ks > 0);
+                    if (C::FL) tc::mma_bf16(cross, f + (OPB >> 4), s, idesc, C::SL || i > 0 || ks > 0);
                 }
-                tc::mma_bf16(tmem + acc * C::BN, f, s, idesc, count++ > 0);
-                if (C::SL) tc::mma_bf16(cross, f, s + (C::SECOND >> 4), idesc, i > 0 || ks > 0);
-                if (C::FL) tc::mma_bf16(cross, f + (OPB >> 4), s, idesc, C::SL || i > 0 || ks > 0);
             }
             tc::commit(&bars->empty[slot]);
         }
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_con
         }
     } else if (warp == 1) {
         if (lane == 0) issue(std::integral_constant<int, 0>());
-    } else if (C::ISSUERS > 1 && warp == 2) {
+    } else if (warp == 2) {
         if (lane == 0) issue(std::integral_constant<int, 1>());
     }
     // Epilogue: two groups of four warps, each taking half of the columns; a warp reads the 32 lanes (rows)

@@ -438,6 +438,8 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
     const long long u = blockIdx.x;
     const int dd = d * d, tid = threadIdx.x;
     w0 += (u % H) * dd;
+    griddep_wait();  // the partials; W0 too may be new
+    griddep_launch();
     if (d == D) {
 #pragma unroll
         for (int i = 0; i < DD / 4 / SM_TPB; ++i) {
@@ -450,8 +452,6 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
             W[r * FLD + c] = r < d && c < d ? __ldg(w0 + r * d + c) : 0.f;
         }
     }
-    griddep_wait();  // the partials
-    griddep_launch();
     part += u * S * 2 * dd;
     const int tr = (tid >> 4) * 4, tc = (tid & 15) * 4;  // rows tr .. + 3, columns tc .. + 3
     float acc[4][4];  // -C first, from C^T

@@ -3,8 +3,11 @@
 Tolerance of the iteration.  Every step rounds its products to about d = 2^-22 of their norm (fp32 sums
 of operands held to 22 bits or more), and a step enlarges what is already wrong by at most a = 3.4445.
 With |X_0| = 1 five steps leave at most 5 a^5 d = 5.8e-4 in the Frobenius norm in the worst direction, and
-the result has norm about sqrt(r), r the rank: TOL / sqrt(r) of it.  A bf16 result adds its own rounding,
-2^-8 of each value.
+the result has norm about sqrt(r), r the rank: TOL / sqrt(r) of it.  A bf16 result may be half a step,
+2^-8, of each value off.  Rounding takes 2^-8 / sqrt(3) of that on average (2.3e-3 at most, values being
+spread over their binades 1.7e-3); X and P of bf16 matrices are held in 11 bits, 2^-11 / sqrt(3) = 2.8e-4
+of the norm each at each of five steps: 5 x 2 x 2.8e-4 = 2.8e-3 if all added up, sqrt(10) x 2.8e-4 = 0.9e-3
+as independent errors.  The root of the squares, 2.5e-3 at the most, is inside 2^-8 = 3.9e-3.
 """
 import math
 
