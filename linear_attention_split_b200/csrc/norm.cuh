@@ -17,6 +17,7 @@
 namespace lnorm {
 
 constexpr int THREADS = 256;    // threads of a block with rows of up to 8 warps; wider rows take one block each
+constexpr int THREADS_BWD = 512;  // of the backward pass, one block an SM (half the partial sums of two blocks of 256)
 constexpr int MAX_EPT = 16;     // elements of a row that one thread holds at most
 constexpr int MAX_COLS = 1024 * MAX_EPT;
 constexpr int STRANDS = 32;     // of the sum over blocks
@@ -164,34 +165,66 @@ __global__ void __launch_bounds__(MAXT)
 }
 
 // ----------------------------------------------------------------------------- backward --
-// Each group of threads walks rows `group, group + groups, ...`, the next row's loads in flight while
-// one is worked on, and keeps its columns' sums of dy xh and dy in registers; the block adds its
-// groups' sums in order and writes one partial row of each, part[block][2][C].
+// Each group of threads walks rows `group, group + groups, ...` and keeps its columns' sums of dy xh
+// and dy in registers; the block adds its groups' sums in order and writes one partial row of each,
+// part[block][2][C].  The next DEPTH - 1 rows are on their way into shared memory by asynchronous copies,
+// each thread fetching what it will read itself (no barrier); 2-byte loads and the widest rows, which have
+// no such copies or no room, keep one row ahead in registers.
+template <typename T, int VEC, int NV, int MAXT>
+struct Ahead {
+    static constexpr int BYTES = NV * VEC * (int)sizeof(T);  // of a thread, per tensor and row
+    static constexpr bool ASYNC = VEC * sizeof(T) >= 4 && MAXT <= 512;
+    static constexpr int DEPTH = BYTES <= 48 ? 4 : 3;
+    static constexpr int smem(int threads) { return ASYNC ? DEPTH * 2 * BYTES * threads : 0; }
+};
+__device__ __forceinline__ void copy_ahead(uint32_t to, const void* from, int bytes) {
+    if (bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+
 template <typename T, int VEC, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == THREADS ? 2 : 1)
     backward_kernel(const T* dy, const T* x, const float* __restrict__ gamma, T* dx, float* __restrict__ part, int rows,
                     int C, float eps, float inv_c, const Shape s) {
     using L = Pack<T, VEC>;
-    extern __shared__ float sums[];  // [rows_per_block][2][C] when a block holds several rows
+    using A = Ahead<T, VEC, NV, MAXT>;
+    extern __shared__ __align__(16) uint8_t smem[];  // rows on their way; then [rows_per_block][2][C] sums
+    float* sums = reinterpret_cast<float*>(smem);
     __shared__ float red[2][5 * 32];
     const int tpr = s.lanes * s.warps, rpb = s.rows_per_block();
     const int at = threadIdx.x % tpr, grp = threadIdx.x / tpr;
     griddep_wait();
     griddep_launch();
     L rx[NV], rt[NV];
-    auto fetch = [&](long long row) {
+    // [slot][tensor][vector][thread]
+    auto place = [&](int slot, int tensor, int i) { return ((slot * 2 + tensor) * NV + i) * s.threads + (int)threadIdx.x; };
+    auto fetch = [&](long long row, int slot) {
+        if (row < rows)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (at + i * tpr) * VEC;
-            if (row < rows && c < C) {
-                rx[i] = *reinterpret_cast<const L*>(x + row * C + c);
-                rt[i] = *reinterpret_cast<const L*>(dy + row * C + c);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (at + i * tpr) * VEC;
+                if (c >= C) continue;
+                if constexpr (A::ASYNC) {
+                    copy_ahead(smem_u32(smem) + place(slot, 0, i) * (uint32_t)sizeof(L), x + row * C + c, sizeof(L));
+                    copy_ahead(smem_u32(smem) + place(slot, 1, i) * (uint32_t)sizeof(L), dy + row * C + c, sizeof(L));
+                } else {
+                    rx[i] = *reinterpret_cast<const L*>(x + row * C + c);
+                    rt[i] = *reinterpret_cast<const L*>(dy + row * C + c);
+                }
             }
-        }
+        if constexpr (A::ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const long long stride = (long long)gridDim.x * rpb;
     long long r0 = (long long)blockIdx.x * rpb;
-    fetch(r0 + grp);
+    if constexpr (A::ASYNC) {
+#pragma unroll
+        for (int d = 0; d < A::DEPTH - 1; ++d) fetch(r0 + grp + d * stride, d);
+    } else {
+        fetch(r0 + grp, 0);
+    }
+    int slot = 0;
     float g[NV][VEC], dg[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -209,6 +242,17 @@ __global__ void __launch_bounds__(MAXT, MAXT == THREADS ? 2 : 1)
         const bool live = row < rows;
         float v[NV][VEC], t[NV][VEC];
         float s1[1] = {0.f};
+        if constexpr (A::ASYNC) {
+            // the slot freed by the last row takes the row DEPTH - 1 ahead; then this row's copies are over
+            fetch(row + (A::DEPTH - 1) * stride, slot == 0 ? A::DEPTH - 1 : slot - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(A::DEPTH - 1) : "memory");
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                rx[i] = reinterpret_cast<const L*>(smem)[place(slot, 0, i)];
+                rt[i] = reinterpret_cast<const L*>(smem)[place(slot, 1, i)];
+            }
+            slot = slot + 1 == A::DEPTH ? 0 : slot + 1;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (live && (at + i * tpr) * VEC < C) {
@@ -221,7 +265,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == THREADS ? 2 : 1)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s1[0] += v[i][e];
         }
-        fetch(row + stride);
+        if constexpr (!A::ASYNC) fetch(row + stride, 0);
         row_sum<1>(s1, s, red[turn]);
         const float mean = s1[0] * inv_c;
         float s4[4] = {0.f, 0.f, 0.f, 0.f};  // c, c^2, t, t c
@@ -263,17 +307,28 @@ __global__ void __launch_bounds__(MAXT, MAXT == THREADS ? 2 : 1)
             }
     }
     float* p = part + (long long)blockIdx.x * 2 * C;
-    if (rpb > 1) {
+    auto put = [&](float* to, const float (&v)[NV][VEC]) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (at + i * tpr) * VEC;
             if (c >= C) continue;
+            if constexpr (VEC % 4 == 0) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                sums[grp * 2 * C + c + e] = dg[i][e];
-                sums[grp * 2 * C + C + c + e] = db[i][e];
+                for (int e = 0; e < VEC; e += 4)
+                    *reinterpret_cast<float4*>(to + c + e) = make_float4(v[i][e], v[i][e + 1], v[i][e + 2], v[i][e + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) to[c + e] = v[i][e];
             }
         }
+    };
+    if (rpb > 1) {
+        if constexpr (A::ASYNC) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();  // every thread has read its last row: the sums may go over them
+        }
+        put(sums + grp * 2 * C, dg);
+        put(sums + grp * 2 * C + C, db);
         __syncthreads();
         for (int c = threadIdx.x; c < 2 * C; c += blockDim.x) {
             float a = 0.f;
@@ -282,16 +337,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == THREADS ? 2 : 1)
             p[c] = a;
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (at + i * tpr) * VEC;
-            if (c >= C) continue;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                p[c + e] = dg[i][e];
-                p[C + c + e] = db[i][e];
-            }
-        }
+        put(p, dg);
+        put(p + C, db);
     }
 }
 
@@ -306,7 +353,7 @@ __global__ void __launch_bounds__(32 * STRANDS)
     griddep_launch();
     float a = 0.f;
     if (col < 2 * C)
-#pragma unroll 10
+#pragma unroll 5
         for (int b = strand; b < blocks; b += STRANDS) a += part[(long long)b * 2 * C + col];
     sm[strand][threadIdx.x & 31] = a;
     __syncthreads();

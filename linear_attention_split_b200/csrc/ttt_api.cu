@@ -841,12 +841,19 @@ int norm_dispatch(const NormPlan& p, int dtype, F f) {
         return p.vec == 8 ? by_nv(__nv_bfloat16(), integral_constant<int, 8>()) : by_nv(__nv_bfloat16(), integral_constant<int, 1>());
     return p.vec == 4 ? by_nv(float(), integral_constant<int, 4>()) : by_nv(float(), integral_constant<int, 1>());
 }
-// blocks of the backward pass: two per SM, fewer for few rows
-int norm_bwd_blocks(const NormPlan& p, int rows) {
+// The backward pass takes blocks of 512 threads, one per SM, or while that would leave SMs without rows
+// blocks of 256, two per SM.
+int norm_bwd_blocks(NormPlan& p, int rows) {
     DeviceInfo* dev = nullptr;
     const int sms = current_device(&dev) == TTT_OK ? dev->sms : 148;
+    const int tpr = p.s.lanes * p.s.warps, wide = lnorm::THREADS_BWD / tpr;
+    int per_sm = 2;
+    if (tpr >= lnorm::THREADS_BWD || rows >= (long long)sms * wide) {
+        p.s.threads = std::max(wide, 1) * tpr;
+        per_sm = 1;
+    }
     const int rpb = p.s.rows_per_block();
-    return std::min(2 * sms, (rows + rpb - 1) / rpb);
+    return std::min(per_sm * sms, (rows + rpb - 1) / rpb);
 }
 int norm_check(const void* a, const void* b, const void* c, const float* gamma, int rows, int C, float eps, int dtype) {
     if (!a || !b || !c || !gamma) return TTT_ERR_INVALID_ARG;
@@ -1701,7 +1708,8 @@ int ttt_layernorm(const void* x, const float* gamma, const float* beta, void* y,
 
 size_t ttt_layernorm_bwd_workspace_bytes(int rows, int C, int dtype) {
     if (rows <= 0 || C <= 0 || C > lnorm::MAX_COLS) return 0;
-    return (size_t)norm_bwd_blocks(norm_plan(C, dtype), rows) * 2 * C * 4;
+    NormPlan p = norm_plan(C, dtype);
+    return (size_t)norm_bwd_blocks(p, rows) * 2 * C * 4;
 }
 
 int ttt_layernorm_bwd(const void* dy, const void* x, const float* gamma, void* dx, float* dgamma, float* dbeta, int rows,
@@ -1712,14 +1720,19 @@ int ttt_layernorm_bwd(const void* dy, const void* x, const float* gamma, void* d
     const size_t need = ttt_layernorm_bwd_workspace_bytes(rows, C, dtype);
     if (workspace_bytes < need || !workspace) return TTT_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TTT_ERR_INVALID_ARG;
-    const NormPlan p = norm_plan(C, dtype);
+    NormPlan p = norm_plan(C, dtype);
     const int blocks = norm_bwd_blocks(p, rows), rpb = p.s.rows_per_block();
-    const int smem = rpb > 1 ? rpb * 2 * C * 4 : 0;
+    const int sums = rpb > 1 ? rpb * 2 * C * 4 : 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     float* part = static_cast<float*>(workspace);
     return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv, auto maxt) {
         using T = decltype(t);
-        if (int rc = launch_pdl(lnorm::backward_kernel<T, vec(), nv(), maxt()>, dim3((unsigned)blocks), p.s.threads, smem, st,
+        using Ahead = lnorm::Ahead<T, vec(), nv(), maxt()>;
+        const auto kern = lnorm::backward_kernel<T, vec(), nv(), maxt()>;
+        const int smem = std::max(sums, Ahead::smem(p.s.threads));
+        static SmemRecord record;
+        if (!allow_smem(kern, std::max(maxt() * lnorm::MAX_EPT * 2 * 4, Ahead::smem(maxt())), record)) return (int)TTT_ERR_CUDA;
+        if (int rc = launch_pdl(kern, dim3((unsigned)blocks), p.s.threads, smem, st,
                                 static_cast<const T*>(dy), static_cast<const T*>(x), gamma, static_cast<T*>(dx), part, rows, C, eps,
                                 (float)(1.0 / C), p.s))
             return rc;
@@ -1751,8 +1764,8 @@ int ttt_rope(const void* q, const void* k, void* q_out, void* k_out, const float
         if (axis_dims[a] <= 0 || axis_dims[a] % 2 || axis_dims[a] > d - at) return TTT_ERR_INVALID_ARG;
         p.ax.at[a] = at;
         p.ax.dims[a] = axis_dims[a];
-        for (int j = 0; j < axis_dims[a] / 2; ++j)
-            p.turns[at / 2 + j] = std::pow(base, -2.0 * j / axis_dims[a]) / 6.283185307179586476925286766559;
+        const double step = -2.0 * std::log2(base) / axis_dims[a];
+        for (int j = 0; j < axis_dims[a] / 2; ++j) p.turns[at / 2 + j] = std::exp2(step * j) / 6.283185307179586476925286766559;
         at += axis_dims[a];
     }
     if (grid) {
