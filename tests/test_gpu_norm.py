@@ -196,3 +196,27 @@ def test_norm_guard_bands():
             n = t.numel() * t.element_size()
             assert (raw[:margin] == 0xA5).all() and (raw[margin + n:] == 0xA5).all()
         check_forward(x, gamma, beta, raws["y"][1].view(rows, C))
+
+
+def test_norm_past_32_bit_offsets():
+    # 2^31 elements and a few rows: the last rows lie behind what a 32-bit element offset reaches
+    rows, C = 524288 + 37, 4096
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of free device memory")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.empty(rows, C, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    gamma = 1 + 0.1 * torch.randn(C, generator=g, device=DEV)
+    y = ttt.layernorm(x, gamma, None, EPS)
+    ends = [0, 1, 524287, 524288, rows - 1]
+    check_forward(x[ends], gamma, None, y[ends])
+    # x as its own gradient: dx of those rows, and the weight's sum over all of them against torch in 64 bits by pieces
+    dx, dgamma, _ = ttt.layernorm_bwd(x, x, gamma, EPS, with_dbeta=False)
+    small = ttt.layernorm_bwd(x[ends].contiguous(), x[ends].contiguous(), gamma, EPS)[0]
+    assert torch.equal(dx[ends], small)
+    want, size = torch.zeros(C, dtype=torch.float64, device=DEV), torch.zeros(C, dtype=torch.float64, device=DEV)
+    for i in range(0, rows, 32768):
+        terms = x[i:i + 32768].double() * stats(x[i:i + 32768])[0]
+        want += terms.sum(0)
+        size += terms.abs().sum(0) + x[i:i + 32768].double().abs().sum(0)
+    adds = rows / 148 + 256 + 2 * 148 / 8 + 8 + 40  # as above: `chain` of the fewest blocks
+    assert ((dgamma.double() - want).abs() <= adds * U * size).all()

@@ -166,3 +166,14 @@ def test_rope_refusals_on_tensors():
         ttt.rope(q, None, (16, 16), pos=torch.zeros(8, 2, device=DEV))
     with pytest.raises(ValueError):
         ttt.rope(q, None, (16, 16), pos=torch.zeros(9, 2))
+
+
+def test_rope_past_32_bit_offsets():
+    # a line of tokens whose last ones lie behind what a 32-bit element offset reaches; far positions as well
+    N, d = (1 << 25) + 11, 64
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB of free device memory")
+    q = torch.empty(1, 1, N, d, dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(device=DEV).manual_seed(5))
+    got = ttt.rope(q, None, (64,), grid=(N,))
+    at = torch.tensor([0, 1, 12345, (1 << 25) - 1, 1 << 25, N - 1], device=DEV)
+    check(got[:, :, at], q[:, :, at], (64,), at[:, None].double())
