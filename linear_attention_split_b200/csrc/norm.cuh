@@ -78,7 +78,8 @@ __device__ __forceinline__ void row_sum(float (&v)[K], const Shape s, float* red
 
 // ----------------------------------------------------------------------------- forward ---
 // A group of threads takes FLY rows at once: their loads are in flight together, and weight and bias
-// are read once for all of them.
+// are read once for all of them.  Bound by HBM (and the launch when small): 100352 x 64 bf16 in 6.8 us,
+// 3.8 TB/s (25600 x 192 fp32 5.5 TB/s); 196 x 384 bf16 in 2.2 us.
 template <typename T, int VEC, int NV, int FLY, int MAXT>
 __global__ void __launch_bounds__(MAXT)
     forward_kernel(const T* x, const float* __restrict__ gamma, const float* __restrict__ beta, T* y, int rows, int C,
@@ -169,7 +170,8 @@ __global__ void __launch_bounds__(MAXT)
 // and dy in registers; the block adds its groups' sums in order and writes one partial row of each,
 // part[block][2][C].  The next DEPTH - 1 rows are on their way into shared memory by asynchronous copies,
 // each thread fetching what it will read itself (no barrier); 2-byte loads and the widest rows, which have
-// no such copies or no room, keep one row ahead in registers.
+// no such copies or no room, keep one row ahead in registers.  12544 x 384 bf16 in 14.1 us with the second
+// kernel (one row ahead in registers and two blocks of 256 an SM: 16.7); long inputs run at 4.4 TB/s.
 template <typename T, int VEC, int NV, int MAXT>
 struct Ahead {
     static constexpr int BYTES = NV * VEC * (int)sizeof(T);  // of a thread, per tensor and row

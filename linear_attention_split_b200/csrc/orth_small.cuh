@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
 constexpr int D = 64, DD = D * D, ROWB = 128, TILE = TM * ROWB;
 
 // G and C^T of one split of a unit's tokens, bf16, d = 64: [V | K]^T K on the tcgen05 tensor cores.
-// Grid (S, U); part [U][S][2][64][64] (G, C^T).
+// Grid (S, U); part [U][S][2][64][64] (G, C^T).  Bound by HBM: K and V once (32 units of 3136 tokens: 10 us
+// from cold caches, 384 of 196: 13).
 constexpr int G_STAGES = 3, G_THREADS = 64 + 128;  // producer, issuer, four epilogue warps
 constexpr uint32_t IDESC_GRAM = tc::idesc_bf16(128, 64, 1, 1);
 struct GBars {
@@ -375,7 +376,8 @@ __global__ void __launch_bounds__(G_THREADS)
 
 // The same for any d <= 128 and type on the CUDA cores: grid (S, U, blocks of 64 x 64 of the d x 2d
 // sums [G | C]), 256 threads with 4 x 4 values each, 32 tokens at a time through shared memory.
-// part [U][S][2][d][d] (G, C^T).
+// part [U][S][2][d][d] (G, C^T).  Bound by the fp32 pipe; S fills the SMs (fp32 keeps its accuracy, which
+// bf16 operands would not).
 template <typename T>
 __global__ void __launch_bounds__(256)
     gram_kernel(const T* __restrict__ k, const T* __restrict__ v, float* __restrict__ part, int N, int d) {
