@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_con
             }
             tc::commit(&bars->empty[slot]);
         }
-        tc::commit(&bars->done);
+        if (nk > 0) tc::commit(&bars->done);  // nobody waits for a CTA without K blocks
     };
     if (warp == 0) {
         if (lane == 0) {

@@ -54,7 +54,8 @@ def check(got, x, **kw):
 
 SHAPES = [(1, 1, 1), (3, 1, 7), (2, 7, 1), (5, 3, 4), (2, 16, 16), (7, 17, 33), (12, 64, 64), (3, 64, 256), (2, 256, 64), (2, 63, 65),
           (4, 65, 64), (2, 128, 128), (3, 100, 130), (1, 129, 200), (2, 320, 320), (1, 384, 1536), (1, 1000, 72), (1, 513, 520),
-          (65, 32, 32), (1, 64, 4096), (1, 1024, 1024)]
+          (65, 32, 32), (1, 64, 4096), (1, 1024, 1024), (1, 1, 5000), (2, 3, 1000), (1, 5000, 3), (200, 70, 72), (3, 576, 600),
+          (450, 33, 64), (1, 2048, 192)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
