@@ -374,52 +374,96 @@ __global__ void __launch_bounds__(G_THREADS)
     if (warp == 1) tc::dealloc(tmem, 64);
 }
 
-// The same for any d <= 128 and type on the CUDA cores: grid (S, U, blocks of 64 x 64 of the d x 2d
-// sums [G | C]), 256 threads with 4 x 4 values each, 32 tokens at a time through shared memory.
-// part [U][S][2][d][d] (G, C^T).  Bound by the fp32 pipe; S fills the SMs (fp32 keeps its accuracy, which
-// bf16 operands would not).
+// Four adjacent features of row `row` (of `rows`) of a [rows][d] tensor from feature c on, zero outside it.
+// vec: d is a multiple of 4, so that they are one aligned load.
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* base, int row, int rows, int c, int d, bool vec) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (row < rows) {
+        const T* at = base + (long long)row * d + c;
+        if (vec) {
+            if (c < d) {
+                struct alignas(4 * sizeof(T)) Lane {
+                    T v[4];
+                };
+                const Lane l = *reinterpret_cast<const Lane*>(at);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = to_f(l.v[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < d) v[e] = to_f(at[e]);
+        }
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void outer4(float (&acc)[4][4], float4 a, float4 b) {
+    const float ax[4] = {a.x, a.y, a.z, a.w}, bx[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ax[i], bx[j], acc[i][j]);
+}
+
+// The same for any d <= 128 and type on the CUDA cores: grid (S, U, blocks of 64 x 64 of the d x d
+// products), 256 threads with 4 x 4 values of G and of C each, 32 tokens at a time through shared memory,
+// the next 32 on their way in registers.  part [U][S][2][d][d] (G, C^T).  Bound by the fp32 pipe; S fills the
+// SMs (fp32 keeps its accuracy, which bf16 operands would not).
 template <typename T>
 __global__ void __launch_bounds__(256)
     gram_kernel(const T* __restrict__ k, const T* __restrict__ v, float* __restrict__ part, int N, int d) {
-    __shared__ float ks[32][68], xs[32][68];
+    constexpr int TOK = 32;
+    __shared__ __align__(16) float tiles[3][TOK][68];  // K's rows of the product, K's and V's columns
     const int S = gridDim.x, r = blockIdx.x;
     const long long u = blockIdx.y;
-    const int nb = (d + 63) / 64, i0 = blockIdx.z / (2 * nb) * 64, jb = blockIdx.z % (2 * nb);
-    const bool is_c = jb >= nb;
-    const int j0 = (is_c ? jb - nb : jb) * 64;
+    const int nb = (d + 63) / 64, i0 = blockIdx.z / nb * 64, j0 = blockIdx.z % nb * 64;
+    const bool vec = d % 4 == 0, same = i0 == j0;
     griddep_wait();
     griddep_launch();
-    const int per = (N + S - 1) / S, t0 = r * per, t1 = min(N, t0 + per);
-    const T* ku = k + u * N * d;
-    const T* xu = (is_c ? v : k) + u * N * d;
-    const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;
-    float acc[4][4] = {};
-    for (int t = t0; t < t1; t += 32) {
-        for (int e = threadIdx.x; e < 32 * 64; e += 256) {
-            const int row = e / 64, c = e % 64;
-            const bool in = t + row < t1;
-            ks[row][c] = in && i0 + c < d ? to_f(ku[(long long)(t + row) * d + i0 + c]) : 0.f;
-            xs[row][c] = in && j0 + c < d ? to_f(xu[(long long)(t + row) * d + j0 + c]) : 0.f;
+    const int per = (N + S - 1) / S, t0 = min(r * per, N), t1 = min(N, t0 + per);
+    const T *ku = k + u * N * d, *vu = v + u * N * d;
+    const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;  // also the place in a tile that a thread fills
+    const int trow = threadIdx.x / 16;
+    float4 next[3][2];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            next[0][h] = load4(ku, t + trow + 16 * h, t1, i0 + tj, d, vec);
+            if (!same) next[1][h] = load4(ku, t + trow + 16 * h, t1, j0 + tj, d, vec);
+            next[2][h] = load4(vu, t + trow + 16 * h, t1, j0 + tj, d, vec);
+        }
+    };
+    float g[4][4] = {}, c[4][4] = {};
+    const int second = same ? 0 : 1;
+    if (t0 < t1) fetch(t0);
+    for (int t = t0; t < t1; t += TOK) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            *reinterpret_cast<float4*>(&tiles[0][trow + 16 * h][tj]) = next[0][h];
+            if (!same) *reinterpret_cast<float4*>(&tiles[1][trow + 16 * h][tj]) = next[1][h];
+            *reinterpret_cast<float4*>(&tiles[2][trow + 16 * h][tj]) = next[2][h];
         }
         __syncthreads();
+        if (t + TOK < t1) fetch(t + TOK);
 #pragma unroll 8
-        for (int row = 0; row < 32; ++row) {
-            const float4 a = *reinterpret_cast<const float4*>(&ks[row][ti]), b = *reinterpret_cast<const float4*>(&xs[row][tj]);
-            const float ax[4] = {a.x, a.y, a.z, a.w}, bx[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ax[i], bx[j], acc[i][j]);
+        for (int row = 0; row < TOK; ++row) {
+            const float4 a = *reinterpret_cast<const float4*>(&tiles[0][row][ti]);
+            outer4(g, a, *reinterpret_cast<const float4*>(&tiles[second][row][tj]));
+            outer4(c, a, *reinterpret_cast<const float4*>(&tiles[2][row][tj]));
         }
         __syncthreads();
     }
-    float* p = part + (u * S + r) * 2 * d * d + (is_c ? (long long)d * d : 0);
+    float* p = part + (u * S + r) * 2 * d * d;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = i0 + ti + i, col = j0 + tj + j;
-            if (row < d && col < d) p[is_c ? (long long)col * d + row : (long long)row * d + col] = acc[i][j];
+            if (row < d && col < d) {
+                p[(long long)row * d + col] = g[i][j];
+                p[(long long)d * d + (long long)col * d + row] = c[i][j];
+            }
         }
 }
 
@@ -462,7 +506,7 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
         float4 g4[4], c4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) g4[i] = c4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
         for (int q = 0; q < S; ++q) {
             const float4* p4 = reinterpret_cast<const float4*>(part + (size_t)q * 2 * DD);
             float4 x[4], y[4];
@@ -484,22 +528,24 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
             acc[0][i] = -c4[i].x, acc[1][i] = -c4[i].y, acc[2][i] = -c4[i].z, acc[3][i] = -c4[i].w;
         }
     } else {
-        for (int e = tid; e < DD; e += SM_TPB) {
-            const int r = e / D, c = e % D;
-            float s = 0.f;
-            if (r < d && c < d)
-                for (int i = 0; i < S; ++i) s += part[(size_t)i * 2 * dd + r * d + c];
-            G[r * FLD + c] = s;
+        float g1[DD / SM_TPB], c1[4][4];
+#pragma unroll
+        for (int i = 0; i < DD / SM_TPB; ++i) g1[i] = c1[i / 4][i % 4] = 0.f;
+        for (int q = 0; q < S; ++q) {
+            const float* p1 = part + (size_t)q * 2 * dd;
+#pragma unroll
+            for (int i = 0; i < DD / SM_TPB; ++i) {
+                const int e = tid + i * SM_TPB, r = e / D, c = e % D, gi = tr + i / 4, gj = tc + i % 4;
+                g1[i] += r < d && c < d ? __ldg(p1 + r * d + c) : 0.f;
+                c1[i / 4][i % 4] += gi < d && gj < d ? __ldg(p1 + dd + gj * d + gi) : 0.f;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float s = 0.f;
-                if (tr + i < d && tc + j < d)
-                    for (int q = 0; q < S; ++q) s += part[((size_t)q * 2 + 1) * dd + (tc + j) * d + tr + i];
-                acc[i][j] = -s;
-            }
+        for (int i = 0; i < DD / SM_TPB; ++i) {
+            const int e = tid + i * SM_TPB;
+            G[(e / D) * FLD + e % D] = g1[i];
+            acc[i / 4][i % 4] = -c1[i / 4][i % 4];
+        }
     }
     __syncthreads();
     float gw[4][4] = {};
@@ -550,43 +596,68 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
     m.end();
 }
 
-// O = Q W on the CUDA cores for any d <= 128 and type: 64 tokens x 64 output features per block,
-// 4 x 4 values a thread, 32 input features at a time through shared memory.  Grid (token tiles, U,
-// feature tiles).
+// O = Q W on the CUDA cores for any d <= 128 and type: 64 tokens x 64 output features per block, 4 x 4
+// values a thread, 64 input features at a time through shared memory (both operands read four features of
+// k at a time: eight 16-byte reads for 64 multiply-adds).  Grid (token tiles, U, feature tiles).
 template <typename T>
 __global__ void __launch_bounds__(256)
     apply_kernel(const T* __restrict__ q, const float* __restrict__ w, T* __restrict__ out, int N, int d) {
-    __shared__ float qs[32][68], ws[32][68];
+    __shared__ __align__(16) float qs[64][68], ws[64][68];  // [token][k], [k][feature]
     const long long u = blockIdx.y;
     const int t0 = blockIdx.x * 64, j0 = blockIdx.z * 64;
-    const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;
+    const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4, row = threadIdx.x / 16;
+    const bool vec = d % 4 == 0;
     griddep_wait();
     griddep_launch();
+    const T* qu = q + u * N * d;
+    const float* wu = w + u * d * d;
     float acc[4][4] = {};
-    for (int k0 = 0; k0 < d; k0 += 32) {
-        for (int e = threadIdx.x; e < 32 * 64; e += 256) {
-            const int t = e / 32, c = e % 32;
-            qs[c][t] = t0 + t < N && k0 + c < d ? to_f(q[(u * N + t0 + t) * d + k0 + c]) : 0.f;
-            const int r = e / 64, j = e % 64;
-            ws[r][j] = k0 + r < d && j0 + j < d ? w[u * d * d + (long long)(k0 + r) * d + j0 + j] : 0.f;
+    for (int k0 = 0; k0 < d; k0 += 64) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            a[h] = load4(qu, t0 + row + 16 * h, N, k0 + tj, d, vec);
+            b[h] = load4(wu, k0 + row + 16 * h, d, j0 + tj, d, vec);
+        }
+        if (k0 > 0) __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            *reinterpret_cast<float4*>(&qs[row + 16 * h][tj]) = a[h];
+            *reinterpret_cast<float4*>(&ws[row + 16 * h][tj]) = b[h];
         }
         __syncthreads();
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float4 a = *reinterpret_cast<const float4*>(&qs[k][ti]), b = *reinterpret_cast<const float4*>(&ws[k][tj]);
-            const float ax[4] = {a.x, a.y, a.z, a.w}, bx[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll 4
+        for (int k = 0; k < 64; k += 4) {
+            float4 x[4], y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ax[i], bx[j], acc[i][j]);
+            for (int i = 0; i < 4; ++i) {
+                x[i] = *reinterpret_cast<const float4*>(&qs[ti + i][k]);
+                y[i] = *reinterpret_cast<const float4*>(&ws[k + i][tj]);
+            }
+            outer4(acc, make_float4(x[0].x, x[1].x, x[2].x, x[3].x), y[0]);
+            outer4(acc, make_float4(x[0].y, x[1].y, x[2].y, x[3].y), y[1]);
+            outer4(acc, make_float4(x[0].z, x[1].z, x[2].z, x[3].z), y[2]);
+            outer4(acc, make_float4(x[0].w, x[1].w, x[2].w, x[3].w), y[3]);
         }
-        __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + ti + i;
+        if (t >= N) break;
+        T* o = out + (u * N + t) * d + j0 + tj;
+        if (vec) {
+            struct alignas(4 * sizeof(T)) Lane {
+                T v[4];
+            } l;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (t0 + ti + i < N && j0 + tj + j < d) out[(u * N + t0 + ti + i) * d + j0 + tj + j] = from_f<T>(acc[i][j]);
+            for (int e = 0; e < 4; ++e) l.v[e] = from_f<T>(acc[i][e]);
+            if (j0 + tj < d) *reinterpret_cast<Lane*>(o) = l;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j0 + tj + e < d) o[e] = from_f<T>(acc[i][e]);
+        }
+    }
 }
 
 // ---- d > 64: the steps of the general path between these two

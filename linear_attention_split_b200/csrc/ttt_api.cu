@@ -1121,10 +1121,10 @@ LinOrthPlan lin_orth_plan(long long U, int N, int d, int dtype) {
         p.S = b.S;
         p.TT = b.TT;
         p.n_tiles = b.n_tiles;
-    } else {  // blocks of at least 64 tokens, about four per SM
+    } else {  // blocks of at least 64 tokens, about two per SM
         const int nb = (d + 63) / 64;
         p.S = 1;
-        while (p.S < 16 && U * p.S * 2 * nb * nb < 4LL * sms && N >= 128 * p.S) p.S *= 2;
+        while (p.S < 16 && U * p.S * nb * nb < 2LL * sms && N >= 128 * p.S) p.S *= 2;
     }
     const size_t dd = (size_t)d * d;
     p.part = 0;
@@ -1156,7 +1156,7 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
                                 tk, part, p.TT, p.n_tiles))
             return rc;
     } else {
-        if (int rc = launch_pdl(orth::gram_kernel<T>, dim3((unsigned)p.S, (unsigned)U, 2 * nb * nb), 256, 0, st,
+        if (int rc = launch_pdl(orth::gram_kernel<T>, dim3((unsigned)p.S, (unsigned)U, nb * nb), 256, 0, st,
                                 static_cast<const T*>(k), static_cast<const T*>(v), part, N, d))
             return rc;
     }
