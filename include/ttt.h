@@ -255,7 +255,8 @@ size_t ttt_linear_chunked_bidir_noalloc_max_bytes(void);
  * with NS the Newton-Schulz steps of ttt_orthogonalize (same steps, a, b, c, eps, scale 1).
  * Tensors, sizes and w_star as for ttt_linear_fullbatch; the workspace is always needed.  The
  * step's length does not depend on the gradient's: eta 0.02 to 0.5 is usual.  Forward only.
- * Sizes: 1 <= d <= 128, B*H <= 65535.  bf16 with d = 64 runs the tensor-core kernels.
+ * Sizes: 1 <= d <= 128, B*H <= 65535.  bf16 with d a multiple of 8 up to 64 runs the tensor-core
+ * kernels (zeros fill its features up to 64).
  * ------------------------------------------------------------------------------------ */
 size_t ttt_linear_fullbatch_orth_workspace_bytes(int B, int H, int N, int d, int dtype);
 int ttt_linear_fullbatch_orth(const void* q, const void* k, const void* v, const float* w0, void* out,

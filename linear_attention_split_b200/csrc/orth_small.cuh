@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
 // ------------------------------------------------------------------ TTT-Linear, orthogonalised step
 constexpr int D = 64, DD = D * D, ROWB = 128, TILE = TM * ROWB;
 
-// G and C^T of one split of a unit's tokens, bf16, d = 64: [V | K]^T K on the tcgen05 tensor cores.
-// Grid (S, U); part [U][S][2][64][64] (G, C^T).  Bound by HBM: K and V once (32 units of 3136 tokens: 10 us
+// G and C^T of one split of a unit's tokens, bf16, d <= 64 (the tensor maps fill up to 64 features with
+// zeros): [V | K]^T K on the tcgen05 tensor cores.  Grid (S, U); part [U][S][2][64][64] (G, C^T).  Bound by HBM: K and V once (32 units of 3136 tokens: 10 us
 // from cold caches, 384 of 196: 13).
 constexpr int G_STAGES = 3, G_THREADS = 64 + 128;  // producer, issuer, four epilogue warps
 constexpr uint32_t IDESC_GRAM = tc::idesc_bf16(128, 64, 1, 1);
@@ -468,13 +468,15 @@ __global__ void __launch_bounds__(256)
 }
 
 // One block per unit, d <= 64: the partials are added in split order, g = (1/N)(G W0 - C) is formed in
-// fp32 on the CUDA cores (4 x 4 values a thread), orthogonalised, and W* = W0 - eta U written.
+// fp32 on the CUDA cores (4 x 4 values a thread), orthogonalised, and W* = W0 - eta U written, to w_star
+// [U][d][d] and, filled up with zeros, to w_pad [U][64][64] (either may be null).  pd: d of the partials, 64
+// where the tensor cores formed them.
 constexpr int FLD = D + 4;
 constexpr int update_smem_bytes() { return small_smem_bytes(D); }
 template <int PER_SM>
 __global__ void __launch_bounds__(SM_TPB, PER_SM)
-    update_kernel(const float* __restrict__ part, const float* __restrict__ w0, float* __restrict__ w_star, int S, int H, int d,
-                  float inv_n, float eta, int steps, float ca, float cb, float cc, float eps) {
+    update_kernel(const float* __restrict__ part, const float* __restrict__ w0, float* __restrict__ w_star,
+                  float* __restrict__ w_pad, int S, int H, int d, int pd, float inv_n, float eta, int steps, float ca, float cb, float cc, float eps) {
     extern __shared__ uint8_t raw[];
     Small m;
     m.begin(raw, 1);
@@ -498,10 +500,10 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
             W[r * FLD + c] = r < d && c < d ? __ldg(w0 + r * d + c) : 0.f;
         }
     }
-    part += u * S * 2 * dd;
+    part += u * S * 2 * pd * pd;
     const int tr = (tid >> 4) * 4, tc = (tid & 15) * 4;  // rows tr .. + 3, columns tc .. + 3
     float acc[4][4];  // -C first, from C^T
-    if (d == D) {
+    if (pd == D) {
         // G (symmetric: rows are its k) and C^T, a split's loads all in flight
         float4 g4[4], c4[4];
 #pragma unroll
@@ -576,21 +578,24 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
         *reinterpret_cast<uint2*>(at) = hi;
         *reinterpret_cast<uint2*>(at + SM_M * 128) = lo;
     }
-    w_star += u * dd;
-    const float f = -eta / (SX * SP);
     m.steps(1, steps, ca, cb, cc, [&](int r, int c, const float (&v)[16]) {
-        if (r >= d) return;
+        const float f = -eta / (SX * SP);
         if (d == D) {
+            float* to = (w_star ? w_star : w_pad) + u * DD + r * D + c;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const float4 w = __ldg(reinterpret_cast<const float4*>(w0 + r * D + c + e));
-                *reinterpret_cast<float4*>(w_star + r * D + c + e) =
+                *reinterpret_cast<float4*>(to + e) =
                     make_float4(fmaf(f, v[e], w.x), fmaf(f, v[e + 1], w.y), fmaf(f, v[e + 2], w.z), fmaf(f, v[e + 3], w.w));
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (c + e < d) w_star[r * d + c + e] = fmaf(f, v[e], __ldg(w0 + r * d + c + e));
+            for (int e = 0; e < 16; ++e) {
+                const bool in = r < d && c + e < d;
+                const float w = in ? fmaf(f, v[e], __ldg(w0 + r * d + c + e)) : 0.f;
+                if (in && w_star) w_star[u * dd + r * d + c + e] = w;
+                if (w_pad) w_pad[u * DD + r * D + c + e] = w;
+            }
         }
     });
     m.end();

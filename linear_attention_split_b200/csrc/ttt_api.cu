@@ -1107,7 +1107,8 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
 
 // ------------------------------------------------------------------ TTT-Linear, orthogonalised step
 struct LinOrthPlan {
-    bool tc;                       // bf16, d = 64: tensor-core sums and output pass
+    bool tc;                       // bf16, d <= 64 in 16-byte rows: tensor-core sums and output pass
+    int pd;                        // d of the sums, filled up to 64 there
     int S, TT, n_tiles;            // token splits of a unit; tiles of TT tokens (tc)
     size_t part, w, g, ns, total;  // byte offsets of the workspace's parts, and its size
 };
@@ -1115,7 +1116,8 @@ LinOrthPlan lin_orth_plan(long long U, int N, int d, int dtype) {
     LinOrthPlan p = {};
     DeviceInfo* dev = nullptr;
     const int sms = current_device(&dev) == TTT_OK ? dev->sms : 148;
-    p.tc = dtype == TTT_BF16 && d == orth::D;
+    p.tc = dtype == TTT_BF16 && d <= orth::D && d % 8 == 0;
+    p.pd = p.tc ? orth::D : d;
     if (p.tc) {
         const BwdPlan b = bwd_plan(U, N, sms);
         p.S = b.S;
@@ -1126,10 +1128,10 @@ LinOrthPlan lin_orth_plan(long long U, int N, int d, int dtype) {
         p.S = 1;
         while (p.S < 16 && U * p.S * nb * nb < 2LL * sms && N >= 128 * p.S) p.S *= 2;
     }
-    const size_t dd = (size_t)d * d;
+    const size_t dd = (size_t)d * d, pp = (size_t)p.pd * p.pd;
     p.part = 0;
-    p.w = align256((size_t)U * p.S * 2 * dd * 4);
-    p.g = p.w + align256((size_t)U * dd * 4);
+    p.w = align256((size_t)U * p.S * 2 * pp * 4);
+    p.g = p.w + align256((size_t)U * pp * 4);
     p.ns = p.g + (d > orth::SM_M ? align256((size_t)U * dd * 4) : 0);
     p.total = p.ns + (d > orth::SM_M ? orth_plan(U, d, d).total : 0);
     return p;
@@ -1143,13 +1145,15 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
     const LinOrthPlan p = lin_orth_plan(U, N, d, sizeof(T) == 2 ? TTT_BF16 : TTT_F32);
     char* ws = static_cast<char*>(workspace);
     float* part = reinterpret_cast<float*>(ws + p.part);
-    float* w = w_star ? w_star : reinterpret_cast<float*>(ws + p.w);
+    // the W* that the output pass reads: the caller's, unless that is none or has to be filled up
+    float* w = w_star && p.pd == d ? w_star : reinterpret_cast<float*>(ws + p.w);
     const float inv_n = (float)(1.0 / N);
     const int nb = (d + 63) / 64;
     if (p.tc) {
         CUtensorMap tk, tv;
         const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-        if (!tmap_bf16_3d(&tk, k, 64, N, (int)U, p.TT, sw) || !tmap_bf16_3d(&tv, v, 64, N, (int)U, p.TT, sw)) return TTT_ERR_CUDA;
+        if (!tmap_bf16_box(&tk, k, d, N, (int)U, 64, p.TT, sw) || !tmap_bf16_box(&tv, v, d, N, (int)U, 64, p.TT, sw))
+            return TTT_ERR_CUDA;
         static SmemRecord record;
         if (!allow_smem(orth::gram_tc_kernel, orth::g_smem_bytes(), record)) return TTT_ERR_CUDA;
         if (int rc = launch_pdl(orth::gram_tc_kernel, dim3((unsigned)p.S, (unsigned)U), orth::G_THREADS, orth::g_smem_bytes(), st, tv,
@@ -1166,8 +1170,9 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
             const auto kern = orth::update_kernel<per_sm()>;
             static SmemRecord record;
             if (!allow_smem(kern, smem, record)) return TTT_ERR_CUDA;
-            return launch_pdl(kern, dim3((unsigned)U), orth::SM_TPB, smem, st, (const float*)part, w0, w, p.S, H, d, inv_n, eta, steps,
-                              a, b, c, eps);
+            return launch_pdl(kern, dim3((unsigned)U), orth::SM_TPB, smem, st, (const float*)part, w0,
+                              w == w_star || p.pd != d ? w_star : w, p.pd != d ? w : nullptr, p.S, H, d, p.pd, inv_n, eta, steps, a,
+                              b, c, eps);
         };
         if (int rc = U <= 2LL * dev->sms ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 3>())) return rc;
         launched(2);
@@ -1184,8 +1189,8 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
     }
     if (p.tc) {
         CUtensorMap tq, to;
-        if (!tmap_bf16_3d(&tq, q, atc::D, N, (int)U, atc::MT, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !tmap_bf16_3d(&to, out, atc::D, N, (int)U, atc::MT, CU_TENSOR_MAP_SWIZZLE_128B))
+        if (!tmap_bf16_box(&tq, q, d, N, (int)U, atc::D, atc::MT, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !tmap_bf16_box(&to, out, d, N, (int)U, atc::D, atc::MT, CU_TENSOR_MAP_SWIZZLE_128B))
             return TTT_ERR_CUDA;
         static SmemRecord record;
         if (!allow_smem(atc::apply_kernel, atc::smem_bytes(), record)) return TTT_ERR_CUDA;

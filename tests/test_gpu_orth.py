@@ -150,7 +150,9 @@ def linear_orth64(inp, eta, steps=5):
 
 LINEAR = [(1, 1, 196, 64, "bf16"), (2, 3, 197, 64, "bf16"), (64, 2, 49, 64, "bf16"), (3, 1, 3136, 64, "bf16"), (1, 2, 1000, 32, "bf16"),
           (2, 2, 100, 48, "bf16"), (1, 2, 196, 64, "f32"), (2, 2, 333, 32, "f32"), (1, 1, 77, 128, "f32"), (1, 1, 50, 5, "f32"),
-          (5, 3, 640, 64, "f32"), (1, 1, 128, 128, "bf16"), (1, 1, 64, 1, "f32")]
+          (5, 3, 640, 64, "f32"), (1, 1, 128, 128, "bf16"), (1, 1, 64, 1, "f32"),
+          (2, 2, 100, 8, "bf16"), (3, 2, 130, 40, "bf16"), (2, 1, 65, 56, "bf16"), (2, 2, 90, 20, "bf16"), (150, 2, 60, 32, "bf16"),
+          (1, 2, 200, 96, "f32"), (2, 1, 333, 70, "f32"), (2, 2, 65, 33, "f32")]
 
 
 @pytest.mark.parametrize("B,H,N,d,dtype", LINEAR)
@@ -186,13 +188,13 @@ def test_linear_orth_special_cases(dtype, d):
     assert_close(ws, rw.numpy(), torch.float32, "one token W*")
 
 
-@pytest.mark.parametrize("dtype,N", [("bf16", 3136), ("f32", 700)])
-def test_linear_orth_is_deterministic_and_in_bounds(dtype, N):
-    inp = inputs.linear_inputs(2, 3, N, 64, dtype=dtype, seed=8)
+@pytest.mark.parametrize("dtype,N,d", [("bf16", 3136, 64), ("f32", 700, 64), ("bf16", 333, 48), ("bf16", 130, 24), ("f32", 99, 33)])
+def test_linear_orth_is_deterministic_and_in_bounds(dtype, N, d):
+    inp = inputs.linear_inputs(2, 3, N, d, dtype=dtype, seed=8)
     g = {k: v.to(DEV) for k, v in inp.items()}
     want = ttt.linear_fullbatch_orth(g["q"], g["k"], g["v"], g["w0"], eta=0.2)
     margin, nbytes = 65536, g["q"].numel() * g["q"].element_size()
-    nb = ttt.ttt_linear_fullbatch_orth_workspace_bytes(2, 3, N, 64, ttt._DT[g["q"].dtype])
+    nb = ttt.ttt_linear_fullbatch_orth_workspace_bytes(2, 3, N, d, ttt._DT[g["q"].dtype])
     raw = torch.full((2 * margin + nbytes,), 0xA5, dtype=torch.uint8, device=DEV)
     ws = torch.full((2 * margin + nb,), 0xA5, dtype=torch.uint8, device=DEV)
     out = raw[margin:margin + nbytes].view(g["q"].dtype).view(g["q"].shape)
