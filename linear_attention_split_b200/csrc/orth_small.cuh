@@ -408,11 +408,12 @@ __device__ __forceinline__ void outer4(float (&acc)[4][4], float4 a, float4 b) {
 
 // The same for any d <= 128 and type on the CUDA cores: grid (S, U, blocks of 64 x 64 of the d x d
 // products), 256 threads with 4 x 4 values of G and of C each, 32 tokens at a time through shared memory,
-// the next 32 on their way in registers.  part [U][S][2][d][d] (G, C^T).  Bound by the fp32 pipe; S fills the
+// the next 32 on their way in registers.  part [U][S][2][pd][pd] (G, C^T), pd = 64 with zeros for d <= 64, d
+// else.  Bound by the fp32 pipe; S fills the
 // SMs (fp32 keeps its accuracy, which bf16 operands would not).
 template <typename T>
 __global__ void __launch_bounds__(256)
-    gram_kernel(const T* __restrict__ k, const T* __restrict__ v, float* __restrict__ part, int N, int d) {
+    gram_kernel(const T* __restrict__ k, const T* __restrict__ v, float* __restrict__ part, int N, int d, int pd) {
     constexpr int TOK = 32;
     __shared__ __align__(16) float tiles[3][TOK][68];  // K's rows of the product, K's and V's columns
     const int S = gridDim.x, r = blockIdx.x;
@@ -454,29 +455,28 @@ __global__ void __launch_bounds__(256)
         }
         __syncthreads();
     }
-    float* p = part + (u * S + r) * 2 * d * d;
+    float* p = part + (u * S + r) * 2 * pd * pd;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = i0 + ti + i, col = j0 + tj + j;
-            if (row < d && col < d) {
-                p[(long long)row * d + col] = g[i][j];
-                p[(long long)d * d + (long long)col * d + row] = c[i][j];
+            if (row < pd && col < pd) {
+                p[(long long)row * pd + col] = g[i][j];
+                p[(long long)pd * pd + (long long)col * pd + row] = c[i][j];
             }
         }
 }
 
 // One block per unit, d <= 64: the partials are added in split order, g = (1/N)(G W0 - C) is formed in
 // fp32 on the CUDA cores (4 x 4 values a thread), orthogonalised, and W* = W0 - eta U written, to w_star
-// [U][d][d] and, filled up with zeros, to w_pad [U][64][64] (either may be null).  pd: d of the partials, 64
-// where the tensor cores formed them.
+// [U][d][d] and, filled up with zeros, to w_pad [U][64][64] (either may be null).  The partials are 64 x 64.
 constexpr int FLD = D + 4;
 constexpr int update_smem_bytes() { return small_smem_bytes(D); }
 template <int PER_SM>
 __global__ void __launch_bounds__(SM_TPB, PER_SM)
     update_kernel(const float* __restrict__ part, const float* __restrict__ w0, float* __restrict__ w_star,
-                  float* __restrict__ w_pad, int S, int H, int d, int pd, float inv_n, float eta, int steps, float ca, float cb, float cc, float eps) {
+                  float* __restrict__ w_pad, int S, int H, int d, float inv_n, float eta, int steps, float ca, float cb, float cc, float eps) {
     extern __shared__ uint8_t raw[];
     Small m;
     m.begin(raw, 1);
@@ -500,54 +500,33 @@ __global__ void __launch_bounds__(SM_TPB, PER_SM)
             W[r * FLD + c] = r < d && c < d ? __ldg(w0 + r * d + c) : 0.f;
         }
     }
-    part += u * S * 2 * pd * pd;
+    part += u * S * 2 * DD;
     const int tr = (tid >> 4) * 4, tc = (tid & 15) * 4;  // rows tr .. + 3, columns tc .. + 3
     float acc[4][4];  // -C first, from C^T
-    if (pd == D) {
-        // G (symmetric: rows are its k) and C^T, a split's loads all in flight
-        float4 g4[4], c4[4];
+    // G (symmetric: rows are its k) and C^T, a split's loads all in flight
+    float4 g4[4], c4[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g4[i] = c4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 4; ++i) g4[i] = c4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int q = 0; q < S; ++q) {
-            const float4* p4 = reinterpret_cast<const float4*>(part + (size_t)q * 2 * DD);
-            float4 x[4], y[4];
+    for (int q = 0; q < S; ++q) {
+        const float4* p4 = reinterpret_cast<const float4*>(part + (size_t)q * 2 * DD);
+        float4 x[4], y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = __ldg(p4 + tid + i * SM_TPB);
-                y[i] = __ldg(p4 + (DD + (tc + i) * D + tr) / 4);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                g4[i].x += x[i].x, g4[i].y += x[i].y, g4[i].z += x[i].z, g4[i].w += x[i].w;
-                c4[i].x += y[i].x, c4[i].y += y[i].y, c4[i].z += y[i].z, c4[i].w += y[i].w;
-            }
+        for (int i = 0; i < 4; ++i) {
+            x[i] = __ldg(p4 + tid + i * SM_TPB);
+            y[i] = __ldg(p4 + (DD + (tc + i) * D + tr) / 4);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int e = (tid + i * SM_TPB) * 4;
-            *reinterpret_cast<float4*>(G + (e / D) * FLD + e % D) = g4[i];
-            acc[0][i] = -c4[i].x, acc[1][i] = -c4[i].y, acc[2][i] = -c4[i].z, acc[3][i] = -c4[i].w;
+            g4[i].x += x[i].x, g4[i].y += x[i].y, g4[i].z += x[i].z, g4[i].w += x[i].w;
+            c4[i].x += y[i].x, c4[i].y += y[i].y, c4[i].z += y[i].z, c4[i].w += y[i].w;
         }
-    } else {
-        float g1[DD / SM_TPB], c1[4][4];
+    }
 #pragma unroll
-        for (int i = 0; i < DD / SM_TPB; ++i) g1[i] = c1[i / 4][i % 4] = 0.f;
-        for (int q = 0; q < S; ++q) {
-            const float* p1 = part + (size_t)q * 2 * dd;
-#pragma unroll
-            for (int i = 0; i < DD / SM_TPB; ++i) {
-                const int e = tid + i * SM_TPB, r = e / D, c = e % D, gi = tr + i / 4, gj = tc + i % 4;
-                g1[i] += r < d && c < d ? __ldg(p1 + r * d + c) : 0.f;
-                c1[i / 4][i % 4] += gi < d && gj < d ? __ldg(p1 + dd + gj * d + gi) : 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < DD / SM_TPB; ++i) {
-            const int e = tid + i * SM_TPB;
-            G[(e / D) * FLD + e % D] = g1[i];
-            acc[i / 4][i % 4] = -c1[i / 4][i % 4];
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int e = (tid + i * SM_TPB) * 4;
+        *reinterpret_cast<float4*>(G + (e / D) * FLD + e % D) = g4[i];
+        acc[0][i] = -c4[i].x, acc[1][i] = -c4[i].y, acc[2][i] = -c4[i].z, acc[3][i] = -c4[i].w;
     }
     __syncthreads();
     float gw[4][4] = {};
@@ -666,7 +645,20 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- d > 64: the steps of the general path between these two
-// g[u] = (1/N)(G W0[h] - C), the partials added in split order
+// The S partials of a unit added in split order, into the first
+__global__ void __launch_bounds__(TPB) fold_kernel(float* __restrict__ part, int S, int dd2) {
+    float* p = part + (long long)blockIdx.x * S * dd2;
+    const int e = blockIdx.y * TPB + threadIdx.x;
+    griddep_wait();
+    griddep_launch();
+    if (e >= dd2) return;
+    float s = p[e];
+#pragma unroll 8
+    for (int q = 1; q < S; ++q) s += p[(long long)q * dd2 + e];
+    p[e] = s;
+}
+
+// g[u] = (1/N)(G W0[h] - C) from the folded partials, which lie S apart
 __global__ void __launch_bounds__(TPB)
     gradient_kernel(const float* __restrict__ part, const float* __restrict__ w0, float* __restrict__ g, int S, int H, int d,
                     float inv_n) {
@@ -676,15 +668,11 @@ __global__ void __launch_bounds__(TPB)
     griddep_launch();
     if (e >= dd) return;
     const int i = e / d, j = e % d;
-    const float* W0 = w0 + (u % H) * dd;
-    float gw = 0.f, c = 0.f;
-    for (int m = 0; m < d; ++m) {
-        float s = 0.f;
-        for (int q = 0; q < S; ++q) s += part[(u * S + q) * 2 * dd + i * d + m];
-        gw = fmaf(s, W0[m * d + j], gw);
-    }
-    for (int q = 0; q < S; ++q) c += part[((u * S + q) * 2 + 1) * dd + j * d + i];
-    g[u * dd + e] = (gw - c) * inv_n;
+    const float *W0 = w0 + (u % H) * dd, *G = part + u * S * 2 * dd;
+    float gw = 0.f;
+#pragma unroll 8
+    for (int m = 0; m < d; ++m) gw = fmaf(G[i * d + m], W0[m * d + j], gw);
+    g[u * dd + e] = (gw - G[dd + j * d + i]) * inv_n;
 }
 
 // W* = W0[h] - eta U

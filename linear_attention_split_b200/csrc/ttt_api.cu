@@ -1108,7 +1108,8 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
 // ------------------------------------------------------------------ TTT-Linear, orthogonalised step
 struct LinOrthPlan {
     bool tc;                       // bf16, d <= 64 in 16-byte rows: tensor-core sums and output pass
-    int pd;                        // d of the sums, filled up to 64 there
+    bool pad;                      // the output pass reads a W* filled up to 64 x 64
+    int pd;                        // d of the sums, filled up to 64
     int S, TT, n_tiles;            // token splits of a unit; tiles of TT tokens (tc)
     size_t part, w, g, ns, total;  // byte offsets of the workspace's parts, and its size
 };
@@ -1117,7 +1118,8 @@ LinOrthPlan lin_orth_plan(long long U, int N, int d, int dtype) {
     DeviceInfo* dev = nullptr;
     const int sms = current_device(&dev) == TTT_OK ? dev->sms : 148;
     p.tc = dtype == TTT_BF16 && d <= orth::D && d % 8 == 0;
-    p.pd = p.tc ? orth::D : d;
+    p.pad = p.tc && d < orth::D;
+    p.pd = std::max(d, orth::D);
     if (p.tc) {
         const BwdPlan b = bwd_plan(U, N, sms);
         p.S = b.S;
@@ -1146,7 +1148,7 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
     char* ws = static_cast<char*>(workspace);
     float* part = reinterpret_cast<float*>(ws + p.part);
     // the W* that the output pass reads: the caller's, unless that is none or has to be filled up
-    float* w = w_star && p.pd == d ? w_star : reinterpret_cast<float*>(ws + p.w);
+    float* w = w_star && !p.pad ? w_star : reinterpret_cast<float*>(ws + p.w);
     const float inv_n = (float)(1.0 / N);
     const int nb = (d + 63) / 64;
     if (p.tc) {
@@ -1161,7 +1163,7 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
             return rc;
     } else {
         if (int rc = launch_pdl(orth::gram_kernel<T>, dim3((unsigned)p.S, (unsigned)U, nb * nb), 256, 0, st,
-                                static_cast<const T*>(k), static_cast<const T*>(v), part, N, d))
+                                static_cast<const T*>(k), static_cast<const T*>(v), part, N, d, p.pd))
             return rc;
     }
     if (d <= orth::SM_M) {
@@ -1171,13 +1173,17 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
             static SmemRecord record;
             if (!allow_smem(kern, smem, record)) return TTT_ERR_CUDA;
             return launch_pdl(kern, dim3((unsigned)U), orth::SM_TPB, smem, st, (const float*)part, w0,
-                              w == w_star || p.pd != d ? w_star : w, p.pd != d ? w : nullptr, p.S, H, d, p.pd, inv_n, eta, steps, a,
+                              p.pad ? w_star : w, p.pad ? w : nullptr, p.S, H, d, inv_n, eta, steps, a,
                               b, c, eps);
         };
         if (int rc = U <= 2LL * dev->sms ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 3>())) return rc;
         launched(2);
     } else {
         float* g = reinterpret_cast<float*>(ws + p.g);
+        if (p.S > 1) {
+            if (int rc = launch_pdl(orth::fold_kernel, grid_units(U, 2LL * d * d), orth::TPB, 0, st, part, p.S, 2 * d * d)) return rc;
+            launched(1);
+        }
         if (int rc = launch_pdl(orth::gradient_kernel, grid_units(U, (long long)d * d), orth::TPB, 0, st, (const float*)part, w0, g,
                                 p.S, H, d, inv_n))
             return rc;
