@@ -11,7 +11,8 @@
 // The bound is latency: a step is three such products, each waiting for the one before (accumulator
 // out of tensor memory, exchange, rounding to hi + lo, operand written, MMAs; about 1400 cycles).  Several
 // blocks share an SM and fill one another's gaps.  Compiled for two blocks an SM nothing spills (32 units of
-// the TTT-Linear step: 22 us, 20 % less than with three); with more matrices than two blocks an SM hold, three
+// the TTT-Linear step, when measured: 27 us against 30 with three, 22 since); with more matrices than two blocks
+// an SM hold, three
 // make one wave of up to 444 (384 units: 41 us against 51).
 #pragma once
 #include "common.cuh"

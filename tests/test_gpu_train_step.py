@@ -156,3 +156,68 @@ def test_explicit_stream_with_scratch_of_its_own():
         side.synchronize()
         assert torch.equal(out, want) and all(torch.equal(p, q) for p, q in zip((dx, dg, db), wdx))
         del junk
+
+
+def test_calls_from_threads():
+    # the binding releases the interpreter lock during a call, so these overlap on the host as well
+    import threading
+
+    cases = [draw(seed) for seed in range(20, 24)]
+    want = [step(s) for s in cases]
+    torch.cuda.synchronize()
+    got, failed = [None] * len(cases), []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[i] = step(cases[i])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    # the projections are torch's own products, whose kernels may differ by thread; everything else is bitwise
+    for g, w in zip(got, want):
+        for n in w:
+            assert torch.allclose(g[n], w[n], rtol=1e-3, atol=1e-4 * w[n].abs().max().item()), n
+
+
+FIRST = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from linear_attention_split_b200 import ttt
+x = torch.randn(300, 96, device="cuda"); gamma = torch.ones(96, device="cuda"); dy = torch.randn_like(x)
+q = torch.randn(2, 3, 20, 64, device="cuda").bfloat16(); w0 = torch.randn(3, 64, 64, device="cuda") / 8
+m, h = torch.randn(1, 200, 150, device="cuda"), torch.randn(1, 200, 150, device="cuda").bfloat16()
+def run():
+    a, b = ttt.rope(q, q, (32, 32), grid=(4, 5))
+    return [ttt.layernorm(x, gamma), *ttt.layernorm_bwd(dy, x, gamma), a, b, ttt.orthogonalize(m), ttt.orthogonalize(h),
+            ttt.orthogonalize(w0), *ttt.linear_fullbatch_orth(a, b, q, w0, with_w_star=True)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    captured = run()
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(s, t) for s, t in zip(captured, run()))
+assert ttt.device_error() == 0
+print("captured first")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
