@@ -75,24 +75,24 @@ __global__ void __launch_bounds__(THREADS, 4)
     // launched with programmatic stream serialization: the table of a token grid depends on nothing the
     // previous grid wrote, so it overlaps that grid's tail
     if (p.pos) griddep_wait();
-    for (int i = threadIdx.x; i < tn * P; i += THREADS) {
-        const int t = i / P, j = i - t * P, tok = t0 + t;
-        int a = 0;
-        while (a + 1 < p.ax.n && 2 * j >= p.ax.at[a + 1]) ++a;
-        double x;
-        if (p.pos) {
-            x = (double)p.pos[b * p.pos_b + (long long)tok * p.ax.n + a];
-        } else {
-            int cell = tok;
-            for (int c = p.ax.n - 1; c > a; --c) cell /= p.ax.grid[c];
-            x = (double)(cell % p.ax.grid[a]);
+    // a thread keeps its pair (there are at most THREADS), its axis and frequency with it, and walks tokens
+    static_assert(MAX_D / 2 <= THREADS, "a thread for each pair");
+    const int apart = THREADS / P, j0 = threadIdx.x % P, first_t = threadIdx.x / P;
+    if (first_t < apart) {
+        int a = 0, inner = 1;  // cells of one step of the axis, on a token grid
+        while (a + 1 < p.ax.n && 2 * j0 >= p.ax.at[a + 1]) ++a;
+        for (int c = a + 1; c < p.ax.n; ++c) inner *= p.pos ? 1 : p.ax.grid[c];
+        const double turns = p.turns[j0];
+        for (int t = first_t; t < tn; t += apart) {
+            const int tok = t0 + t;
+            const double x = p.pos ? (double)p.pos[b * p.pos_b + (long long)tok * p.ax.n + a] : (double)(tok / inner % p.ax.grid[a]);
+            double r = x * turns;
+            r -= rint(r);
+            float sn, cs;
+            sincospif(2.f * (float)r, &sn, &cs);
+            cosines[t * P + j0] = cs;
+            sines[t * P + j0] = p.sign * sn;
         }
-        double r = x * p.turns[j];
-        r -= rint(r);
-        float sn, cs;
-        sincospif(2.f * (float)r, &sn, &cs);
-        cosines[i] = cs;
-        sines[i] = p.sign * sn;
     }
     if (!p.pos) griddep_wait();
     griddep_launch();
