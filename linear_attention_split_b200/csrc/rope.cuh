@@ -16,9 +16,11 @@
 // The bound is HBM (one read and one write of Q and K).  A thread takes VEC adjacent pairs: two
 // loads of VEC features (16 bytes each where dims, strides and pointers are multiples of 16 bytes;
 // the largest power of two that divides them all otherwise), two table reads, two stores.  A unit
-// (its place in the head) is fixed for a thread; it walks rows, several loads in flight.  Two clips of 8 x
-// 24 x 24 tokens, 12 heads of 128, bf16: 24.8 us, 4.6 TB/s (blocks of 8 or 32 tokens 26.7 and 29.4, three or
-// five blocks an SM 30 and 42).  Sections whose halves are odd go by single features: 1.4 TB/s.
+// (its place in the head) is fixed for a thread; it walks rows, several loads in flight, and finds a row's head
+// and token by shifts (TN is a power of two).  Two clips of 8 x 24 x 24 tokens, 12 heads of 128, bf16: 21.8 us,
+// 5.2 TB/s (22.6 with a division per row, 24.8 with one per entry of the table as well; then blocks of 8 or 32
+// tokens took 26.7 and 29.4, three or five blocks an SM 30 and 42).  Sections whose halves are odd go by
+// single features: 1.5 TB/s.
 #pragma once
 #include "common.cuh"
 
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(THREADS, 4)
     const int unit0 = threadIdx.x % all, r0 = threadIdx.x / all;
     if (r0 >= rpp && all <= THREADS) return;
     const int h0 = blockIdx.y * p.heads, hn = min(p.heads, p.H - h0);
-    const int rows = (k ? 2 : 1) * hn * tn;
+    const int lg = 31 - __clz(p.TN), rows = (k ? 2 : 1) * hn << lg;  // a last tile's missing tokens count as rows
     for (int unit = unit0; unit < all; unit += THREADS) {  // more than one pass only for heads wider than the block
         int e1 = 2 * VEC * unit, e2 = e1 + VEC, j = VEC * unit;
         const bool turned = unit < p.units;
@@ -121,21 +123,21 @@ __global__ void __launch_bounds__(THREADS, 4)
 #pragma unroll
             for (int f = 0; f < FLY; ++f) {
                 const int row = first + f * rpp;
-                if (row >= rows) break;
-                const int hh = row / tn, t = row - hh * tn;
+                const int hh = row >> lg, t = row - (hh << lg);
+                tok[f] = row < rows && t < tn ? t : -1;
+                if (tok[f] < 0) continue;
                 const bool is_k = hh >= hn;
                 const int h = h0 + (is_k ? hh - hn : hh);
                 const View& vi = is_k ? p.ki : p.qi;
                 const View& vo = is_k ? p.ko : p.qo;
                 const T* src = (is_k ? k : q) + b * vi.b + h * vi.h + (t0 + t) * vi.n;
                 dst[f] = (is_k ? kout : qout) + b * vo.b + h * vo.h + (t0 + t) * vo.n;
-                tok[f] = t;
                 x[f] = *reinterpret_cast<const L*>(src + e1);
                 if (turned) y[f] = *reinterpret_cast<const L*>(src + e2);
             }
 #pragma unroll
             for (int f = 0; f < FLY; ++f) {
-                if (first + f * rpp >= rows) break;
+                if (tok[f] < 0) continue;
                 if (!turned) {
                     *reinterpret_cast<L*>(dst[f] + e1) = x[f];
                     continue;
