@@ -12,8 +12,7 @@
 // out of tensor memory, exchange, rounding to hi + lo, operand written, MMAs; about 1400 cycles).  Several
 // blocks share an SM and fill one another's gaps.  Compiled for two blocks an SM nothing spills (32 units of
 // the TTT-Linear step, when measured: 27 us against 30 with three, 22 since); with more matrices than two blocks
-// an SM hold, three
-// make one wave of up to 444 (384 units: 41 us against 51).
+// an SM hold, three make one wave of up to 444 (384 units: 41 us against 51).
 #pragma once
 #include "common.cuh"
 #include "orth.cuh"
