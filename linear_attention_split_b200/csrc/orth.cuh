@@ -9,13 +9,14 @@
 //
 // The products run on the fp16 tensor cores.  An operand is held as hi + lo, two fp16 numbers (about
 // 22 bits), and a product is hi hi + hi lo + lo hi accumulated in fp32.  fp32 matrices take all three
-// (result good to about 2e-6 of its norm).  For bf16 ones X and P are held as hi alone and only the
-// product A Q is taken in full: the iteration enlarges what is lost early by up to a^5, and at s = 1 the
-// polynomial cancels 3.4 - 4.8 + 2.0, so A has to be exact where it meets itself.  In simulation bf16
-// operands leave 3e-2 of the result's norm wrong, hi hi throughout 2e-3 to 3e-3, this choice 0.9e-3 to
-// 1.4e-3, less than the 1.7e-3 that rounding the result to bf16 costs.  Values are bounded (|s| <= 2
-// throughout, checked on the host), so fixed powers of two keep them inside fp16: X and A are stored
-// times 2^12, P times 2^10, Q times 2^9.
+// (result good to about 2e-6 of its norm).  bf16 ones take them too, up to the last step: the iteration
+// enlarges what is lost early by up to a^5 along small singular values, so with X and P in 11 bits at every
+// step a direction 30, 100 or 1000 times the rest left 0.8, 2 or 9 % of the result's norm wrong.  In the last
+// step (the last ones whose slopes multiply to at most 4: orth_high_from) X and P are held as hi alone and only
+// A Q is taken in full, which costs less than rounding the result to bf16, whatever the spectrum (1.5e-3 to
+// 2.3e-3 in all, measured; 1024 x 4096: 240 us, with hi alone at every step 159, in full throughout 263).
+// Values are bounded (|s| <= 2 throughout, checked on the host), so fixed powers of two keep them inside fp16:
+// X and A are stored times 2^12, P times 2^10, Q times 2^9.
 //
 // product_kernel: one tile of 128 x 64, 128 or 256 of a product per cluster; the K range is split over the S
 // CTAs of the cluster when there are few tiles, and the partial tiles are exchanged through

@@ -882,9 +882,11 @@ bool rope_strides_disjoint(const long long* st, int B, int H, int N, int d) {
 // ------------------------------------------------------------------ orthogonal update ---
 // Whether the iteration stays bounded: every value in [0, 1] (the singular values of a matrix of
 // Frobenius norm 1) keeps to at most 2 through all steps, and |b s^2| + |c s^4| to at most 32.
-bool orth_coef_ok(double a, double b, double c, int steps) {
+// slope[k]: the polynomial's largest slope over the values that step k can meet (null: not wanted).
+bool orth_coef_ok(double a, double b, double c, int steps, double* slope = nullptr) {
     double top = 1.0;  // the values reach from 0 to here
     const auto p = [&](double t) { return std::fabs(std::sqrt(t) * (a + t * (b + t * c))); };  // of t = s^2
+    const auto dp = [&](double t) { return std::fabs(a + t * (3.0 * b + t * 5.0 * c)); };
     for (int k = 0; k < steps; ++k) {
         const double t = top * top;
         if (std::fabs(b) * t + std::fabs(c) * t * t > 32.0) return false;
@@ -900,9 +902,24 @@ bool orth_coef_ok(double a, double b, double c, int steps) {
             }
         }
         if (!(next <= 2.0)) return false;
+        if (slope) {
+            slope[k] = std::max(dp(0.0), dp(t));
+            const double at = c == 0.0 ? 0.0 : -3.0 * b / (10.0 * c);
+            if (at > 0.0 && at < t) slope[k] = std::max(slope[k], dp(at));
+        }
         top = next;
     }
     return true;
+}
+// The first step whose X and P a bf16 matrix may hold in one fp16 number.  That rounding is 2^-11 of a value,
+// an eighth of the result's own; the steps from k on enlarge it by the product of their slopes at most, whatever
+// the matrix' spectrum: up to 4, half of the result's rounding, taken of X's norm.  The usual quintic: the last step.
+int orth_high_from(float a, float b, float c, int steps) {
+    double slope[64], gain = 1.0;
+    orth_coef_ok(a, b, c, steps, slope);
+    int k = steps;
+    while (k > 0 && (gain *= slope[k - 1]) <= 4.0) --k;
+    return k;
 }
 struct OrthPlan {
     bool small;  // one block per matrix, no workspace
@@ -990,24 +1007,26 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         return launched(1);
     }
     if (orth_tiles(false, p.M, p.N, 64) > 65535) return TTT_ERR_UNSUPPORTED;
-    constexpr bool kHalf = sizeof(T) == 2;  // bf16: X and P are held in one fp16 number
+    constexpr bool kHalf = sizeof(T) == 2;
+    const int high_from = kHalf ? orth_high_from(a, b, c, steps) : steps;  // from here on X and P are held in one fp16 number
     const long long mn = (long long)m * n;
     char* w = static_cast<char*>(workspace);
     double* part = reinterpret_cast<double*>(w + p.part);
     __half *X = reinterpret_cast<__half*>(w + p.x), *Z = reinterpret_cast<__half*>(w + p.z);
     __half *A = reinterpret_cast<__half*>(w + p.a), *Q = reinterpret_cast<__half*>(w + p.q), *P = reinterpret_cast<__half*>(w + p.p);
 
-    // the three products' tiles
+    // the three products' tiles, in full [0] and of the hi parts alone [1]
     const int kx = (p.N + orth::KB - 1) / orth::KB, km = (p.M + orth::KB - 1) / orth::KB;
-    OrthPick pick[3];
+    OrthPick pick[2][3];
     auto consider = [&](auto bn) {
         constexpr int BN = bn();
-        using C = std::conditional_t<kHalf, orth::High<BN>, orth::Full<BN>>;
         if constexpr (BN <= 128) {
-            orth_consider<C>(pick[0], orth_tiles(true, p.M, p.M, BN), U, kx);
-            orth_consider<orth::Full<BN>>(pick[1], orth_tiles(true, p.M, p.M, BN), U, km);
+            orth_consider<orth::Full<BN>>(pick[0][0], orth_tiles(true, p.M, p.M, BN), U, kx);
+            orth_consider<orth::Full<BN>>(pick[0][1], orth_tiles(true, p.M, p.M, BN), U, km);
+            orth_consider<orth::Full<BN>>(pick[0][2], orth_tiles(false, p.M, p.N, BN), U, km);
+            orth_consider<orth::High<BN>>(pick[1][0], orth_tiles(true, p.M, p.M, BN), U, kx);
         }
-        if constexpr (BN <= 128 || kHalf) orth_consider<C>(pick[2], orth_tiles(false, p.M, p.N, BN), U, km);
+        orth_consider<orth::High<BN>>(pick[1][2], orth_tiles(false, p.M, p.N, BN), U, km);
     };
     consider(std::integral_constant<int, 64>());
     consider(std::integral_constant<int, 128>());
@@ -1017,28 +1036,30 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         return tmap_bf16_box(t, y, ld, p.M, (int)U * 2, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_128B,
                              CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
     };
-    orth::Maps gram[2] = {}, poly = {}, next[2] = {};  // [1]: X is in Z
+    orth::Maps gram[2][2] = {}, poly = {}, next[2] = {};  // gram[hi alone][.]; [1]: X is in Z
     for (int t = 0; t < 2; ++t) {
-        if (!map(&gram[t].first_k, t ? Z : X, p.ldx, orth::KB, orth::TM) ||
-            !map(&gram[t].second_k, t ? Z : X, p.ldx, orth::KB, pick[0].bn) ||
-            !map(&next[t].second_mn, t ? Z : X, p.ldx, 64, orth::KB))
-            return TTT_ERR_CUDA;
+        for (int h = 0; h < (kHalf ? 2 : 1); ++h)
+            if (!map(&gram[h][t].first_k, t ? Z : X, p.ldx, orth::KB, orth::TM) ||
+                !map(&gram[h][t].second_k, t ? Z : X, p.ldx, orth::KB, pick[h][0].bn))
+                return TTT_ERR_CUDA;
+        if (!map(&next[t].second_mn, t ? Z : X, p.ldx, 64, orth::KB)) return TTT_ERR_CUDA;
     }
     if (!map(&poly.first_k, A, p.lda, orth::KB, orth::TM) || !map(&poly.first_mn, A, p.lda, 64, orth::KB) ||
-        !map(&poly.second_k, Q, p.lda, orth::KB, pick[1].bn) || !map(&poly.second_mn, Q, p.lda, 64, orth::KB) ||
+        !map(&poly.second_k, Q, p.lda, orth::KB, pick[0][1].bn) || !map(&poly.second_mn, Q, p.lda, 64, orth::KB) ||
         !map(&next[0].first_k, P, p.lda, orth::KB, orth::TM) || !map(&next[0].first_mn, P, p.lda, 64, orth::KB))
         return TTT_ERR_CUDA;
     next[1].first_k = next[0].first_k;
     next[1].first_mn = next[0].first_mn;
 
+    const int first_parts = high_from == 0 ? 1 : 2;
     if (int rc = launch_pdl(orth::square_kernel<T>, dim3((unsigned)p.parts, (unsigned)U), orth::TPB, 0, st, x, part, mn))
         return rc;
     if (!p.tall && p.N % 8 == 0) {
         if (int rc = launch_pdl(orth::start8_kernel<T>, dim3((unsigned)((mn / 8 + 255) / 256), (unsigned)U), 256, 0, st, x,
-                                (const double*)part, X, p.parts, mn, kHalf ? 1 : 2, eps))
+                                (const double*)part, X, p.parts, mn, first_parts, eps))
             return rc;
     } else if (int rc = launch_pdl(orth::start_kernel<T>, dim3((p.ldx + 31) / 32, (p.M + 31) / 32, (unsigned)U), 256, 0, st, x,
-                                   (const double*)part, X, p.parts, p.M, p.N, p.ldx, p.tall, kHalf ? 1 : 2, eps)) {
+                                   (const double*)part, X, p.parts, p.M, p.N, p.ldx, p.tall, first_parts, eps)) {
         return rc;
     }
     PParams base = {};
@@ -1075,7 +1096,9 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
         return cudaLaunchKernelEx(&cfg, kern, maps, q) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
     };
     // full: the product takes lo parts too
-    auto product = [&](auto full, auto kind, const orth::Maps& maps, const OrthPick& k, const PParams& q) -> int {
+    auto product = [&](auto full, auto kind, const orth::Maps& maps, const PParams& q) -> int {
+        constexpr int at = kind() >= orth::NEXT ? 2 : kind();
+        const OrthPick& k = pick[full() ? 0 : 1][at];
         if constexpr (full()) {
             return k.bn == 64 ? launch(orth::Full<64>(), kind, maps, k.S, q) : launch(orth::Full<128>(), kind, maps, k.S, q);
         } else {
@@ -1084,22 +1107,29 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
             return k.bn == 64 ? launch(orth::High<64>(), kind, maps, k.S, q) : launch(orth::High<128>(), kind, maps, k.S, q);
         }
     };
-    constexpr std::bool_constant<!kHalf> rest;
-    for (int k = 0; k < steps; ++k) {
+    auto step = [&](int k, auto full) -> int {
         const bool odd = k & 1, last = k + 1 == steps;
         PParams q = base;
         q.parts = 2;
         q.y = A;
         q.y2 = Q;
         q.ld = p.lda;
-        if (int rc = product(rest, Kind<orth::GRAM>(), gram[odd], pick[0], q)) return rc;
-        q.parts = kHalf ? 1 : 2;
+        if (int rc = product(full, Kind<orth::GRAM>(), gram[full() ? 0 : 1][odd], q)) return rc;
+        q.parts = full() ? 2 : 1;
         q.y = P;
-        if (int rc = product(std::true_type(), Kind<orth::POLY>(), poly, pick[1], q)) return rc;
+        if (int rc = product(std::true_type(), Kind<orth::POLY>(), poly, q)) return rc;
+        q.parts = k + 1 < high_from ? 2 : 1;
         q.y = odd ? X : Z;
         q.ld = p.ldx;
-        const int rc = last ? product(rest, Kind<kHalf ? orth::OUT_BF16 : orth::OUT_F32>(), next[odd], pick[2], q)
-                            : product(rest, Kind<orth::NEXT>(), next[odd], pick[2], q);
+        return last ? product(full, Kind<kHalf ? orth::OUT_BF16 : orth::OUT_F32>(), next[odd], q)
+                    : product(full, Kind<orth::NEXT>(), next[odd], q);
+    };
+    for (int k = 0; k < steps; ++k) {
+        int rc = TTT_OK;
+        if constexpr (kHalf)
+            rc = k < high_from ? step(k, std::true_type()) : step(k, std::false_type());
+        else
+            rc = step(k, std::true_type());
         if (rc) return rc;
     }
     return launched(2 + 3 * steps);
