@@ -395,6 +395,13 @@ def _sig_type(*sigs):
     return _DT[dtype]
 
 
+def _sig_int(*sizes):
+    """Sizes fit the library's int: ctypes would cut them to 32 bits without a word."""
+    if any(not -2 ** 31 <= n < 2 ** 31 for n in sizes):
+        raise ValueError(f"sizes have to be below 2^31, got {sizes}")
+    return sizes
+
+
 def _sig_vector(sig, C, name):
     if sig is not None and (sig[0] is not torch.float32 or tuple(sig[1]) != (C,) or not _sig_dense(sig)):
         raise ValueError(f"{name} must be a contiguous fp32 tensor [C]")
@@ -454,7 +461,7 @@ def _norm_args(x, gamma, beta, *like_x):
     C = shape[-1] if len(shape) else 0
     _sig_vector(gamma, C, "gamma")
     _sig_vector(beta, C, "beta")
-    return (math.prod(shape[:-1]) if C else 0), C, dt, _sig_device(x, gamma, beta, *like_x)
+    return *_sig_int(math.prod(shape[:-1]) if C else 0, C), dt, _sig_device(x, gamma, beta, *like_x)
 
 
 def _layernorm(x, gamma, beta, y, eps, stream, args):
@@ -477,7 +484,7 @@ def ttt_layernorm(x, gamma, beta, y, eps=1e-6, stream=None):
 
 
 def ttt_layernorm_bwd_workspace_bytes(rows, C, dtype):
-    return lib().ttt_layernorm_bwd_workspace_bytes(rows, C, dtype)
+    return lib().ttt_layernorm_bwd_workspace_bytes(*_sig_int(rows, C), dtype)
 
 
 def ttt_layernorm_bwd(dy, x, gamma, dx, dgamma, dbeta=None, eps=1e-6, workspace=None, stream=None):
@@ -497,7 +504,8 @@ def _rope_args(q, k, q_out, k_out, pos, dims, grid):
         raise ValueError("q, k and their outputs must be [B, H, N, d]")
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}")
-    B, H, N, d = shape
+    B, H, N, d = _sig_int(*shape)
+    _sig_int(*dims, *(grid or ()))
     strides = []
     for t in (q, k, q_out, k_out):
         if t is None:
@@ -542,7 +550,7 @@ def ttt_rope(q, k, q_out, k_out, dims, grid=None, pos=None, base=10000.0, interl
 
 
 def ttt_orthogonalize_workspace_bytes(U, m, n, dtype):
-    return lib().ttt_orthogonalize_workspace_bytes(U, m, n, dtype)
+    return lib().ttt_orthogonalize_workspace_bytes(*_sig_int(U, m, n), dtype)
 
 
 def ttt_orthogonalize(x, out, steps=5, coef=NS_COEF, eps=1e-7, scale=1.0, workspace=None, stream=None):
@@ -557,11 +565,12 @@ def _orth_args(x, *like_x):
     if len(x[1]) < 2:
         raise ValueError("x must be [..., m, n]")
     m, n = x[1][-2:]
-    return math.prod(x[1][:-2]), m, n, dt, _sig_device(x, *like_x)
+    return *_sig_int(math.prod(x[1][:-2]), m, n), dt, _sig_device(x, *like_x)
 
 
 def _orthogonalize(x, out, steps, coef, eps, scale, workspace, stream, args):
     U, m, n, dt, dev = args
+    _sig_int(steps)
     a, b, c = coef
     ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_orthogonalize_workspace_bytes", dev, U, m, n, dt), workspace, dev, stream)
     _call(lib().ttt_orthogonalize, dev, stream, x.data_ptr(), out.data_ptr(), U, m, n, steps, a, b, c, eps, scale, dt, ws, nbytes)
@@ -569,13 +578,14 @@ def _orthogonalize(x, out, steps, coef, eps, scale, workspace, stream, args):
 
 
 def ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dtype):
-    return lib().ttt_linear_fullbatch_orth_workspace_bytes(B, H, N, d, dtype)
+    return lib().ttt_linear_fullbatch_orth_workspace_bytes(*_sig_int(B, H, N, d), dtype)
 
 
 def ttt_linear_fullbatch_orth(q, k, v, w0, out, w_star=None, eta=0.1, steps=5, coef=NS_COEF, eps=1e-7, workspace=None,
                               stream=None):
     """TTT-Linear whose inner step goes along the orthogonalised gradient; tensors as for ttt_linear_fullbatch."""
     B, H, N, d, dt, dev = _linear_orth_args(_sig(q), _sig(k), _sig(v), _sig(out), _sig(w0), _sig(w_star))
+    _sig_int(steps)
     a, b, c = coef
     ws, nbytes, _keep = _scratch(_scratch_bytes("ttt_linear_fullbatch_orth_workspace_bytes", dev, B, H, N, d, dt), workspace, dev,
                                  stream)
@@ -589,7 +599,7 @@ def _linear_orth_args(q, k, v, out, w0, w_star):
     dt = _sig_type(q, k, v, out)
     if len(q[1]) != 4:
         raise ValueError("q, k, v and out must be [B, H, N, d]")
-    B, H, N, d = q[1]
+    B, H, N, d = _sig_int(*q[1])
     for w, shape in ((w0, (H, d, d)), (w_star, (B, H, d, d))):
         if w is not None and (w[0] is not torch.float32 or tuple(w[1]) != shape or not _sig_dense(w)):
             raise ValueError("w0 must be [H, d, d] and w_star [B, H, d, d], contiguous fp32")
