@@ -852,8 +852,8 @@ int norm_bwd_blocks(NormPlan& p, int rows) {
         p.s.threads = std::max(wide, 1) * tpr;
         per_sm = 1;
     }
-    const int rpb = p.s.rows_per_block();
-    return std::min(per_sm * sms, (rows + rpb - 1) / rpb);
+    const long long rpb = p.s.rows_per_block();
+    return (int)std::min<long long>(per_sm * sms, (rows + rpb - 1) / rpb);
 }
 int norm_check(const void* a, const void* b, const void* c, const float* gamma, int rows, int C, float eps, int dtype) {
     if (!a || !b || !c || !gamma) return TTT_ERR_INVALID_ARG;

@@ -66,3 +66,13 @@ def test_workspace_queries():
                  lambda: ttt.ttt_linear_fullbatch_orth_workspace_bytes(1, 1, 2 ** 32 + 16, 64, 1)):
         with pytest.raises(ValueError, match=TOO_LARGE):
             call()
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("C", [1, 8, 64, 384, 1000, 16384])
+def test_layernorm_bwd_workspace_of_the_most_rows(C, dtype):
+    # two blocks an SM at most, of which each leaves two rows of C sums
+    few = ttt.ttt_layernorm_bwd_workspace_bytes(2 ** 24, C, dtype)
+    assert 0 < few <= 2 * 256 * 2 * C * 4
+    for rows in (2 ** 31 - 600, 2 ** 31 - 512, 2 ** 31 - 256, 2 ** 31 - 2, 2 ** 31 - 1):
+        assert ttt.ttt_layernorm_bwd_workspace_bytes(rows, C, dtype) == few
