@@ -254,7 +254,8 @@ size_t ttt_linear_chunked_bidir_noalloc_max_bytes(void);
  *     g  = (1/N) (K^T K W0[h] - K^T V),   W* = W0[h] - eta * NS(g),   O = Q W*,
  * with NS the Newton-Schulz steps of ttt_orthogonalize (same steps, a, b, c, eps, scale 1).
  * Tensors, sizes and w_star as for ttt_linear_fullbatch; the workspace is always needed.  The
- * step's length does not depend on the gradient's: eta 0.02 to 0.5 is usual.  Forward only.
+ * step's length does not depend on the gradient's: eta 0.02 to 0.5 is usual.  Forward only.  Equal calls
+ * give equal bits; with another B*H a unit's tokens may be split and added otherwise.
  * Sizes: 1 <= d <= 128, B*H <= 65535.  bf16 with d a multiple of 8 up to 64 runs the tensor-core
  * kernels (zeros fill its features up to 64).
  * ------------------------------------------------------------------------------------ */
@@ -284,7 +285,9 @@ int ttt_linear_fullbatch_orth(const void* q, const void* k, const void* v, const
  * steps outside 1..64, eps <= 0 or a non-finite number is TTT_ERR_INVALID_ARG; coefficients under
  * which a value in [0, 1] leaves [-2, 2] on the way (the iteration would run away), U > 65535,
  * m or n > 32768, or more than 65535 tiles of 128 rows by 64 columns (shorter side by longer) is
- * TTT_ERR_UNSUPPORTED.  Matrices of at most 64 by 256 (or 256 by 64) need no workspace.
+ * TTT_ERR_UNSUPPORTED.  Matrices of at most 64 by 256 (or 256 by 64) need no workspace, and their
+ * results are the same bit for bit whatever U; larger ones may be cut into other tiles in another
+ * batch, with results that differ within the bounds above.  Equal calls give equal bits.
  * ------------------------------------------------------------------------------------ */
 size_t ttt_orthogonalize_workspace_bytes(int U, int m, int n, int dtype);
 int ttt_orthogonalize(const void* x, void* out, int U, int m, int n, int steps, float a, float b, float c,
