@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(256)
 constexpr int TM = 128, KB = 64;                     // rows of a tile of the output, K block
 constexpr int PANEL = 64 * KB * 2;                   // a K block of 64 rows or columns, 8 KB
 constexpr int OPB = 2 * PANEL;                       // the first operand's K block
-constexpr int MAX_SPLIT = 8;
 constexpr float SQ = 512.f;                          // scale of stored Q
 
 enum Kind { GRAM = 0, POLY = 1, NEXT = 2, OUT_F32 = 3, OUT_BF16 = 4 };

@@ -43,7 +43,7 @@ struct View {              // element strides; the features of a head are adjace
 struct Params {
     const float* pos;      // [N][axes] or [B][N][axes], or null: the grid in raster order
     long long pos_b;       // stride of a batch entry, 0 when shared
-    int B, H, N, d, TN;
+    int H, N, TN;
     int heads;             // heads of a block
     int units, tail;       // units of a head: pairs / VEC turned, then tail / VEC passed on
     int interleaved;

@@ -799,7 +799,7 @@ NormPlan norm_plan(int C, int dtype) {
     p.vec = C % full == 0 ? full : 1;
     const int vecs = C / p.vec, most = lnorm::MAX_EPT / p.vec;
     p.nv = most;
-    while (p.nv > 1 && p.nv * 16 > vecs) p.nv = p.nv == 12 ? 8 : p.nv / 2;  // short rows: a lane per vector first
+    while (p.nv > 1 && p.nv * 16 > vecs) p.nv /= 2;  // short rows: a lane per vector first
     if (p.nv == 16 && (vecs + 31) / 32 <= 12) p.nv = 12;
     const int need = (vecs + p.nv - 1) / p.nv;
     if (need <= 32) {
@@ -814,14 +814,18 @@ NormPlan norm_plan(int C, int dtype) {
     p.s.threads = tpr >= lnorm::THREADS ? tpr : lnorm::THREADS / tpr * tpr;
     return p;
 }
-// f(type, elements of a load, loads of a thread, threads of a block at most)
-template <typename F>
+// f(type, elements of a load, loads of a thread, threads of a block at most).  Rows of more than a warp hold the
+// most elements a thread, so other kernels have blocks of THREADS, in the backward pass THREADS_BWD as well.
+template <bool BWD, typename F>
 int norm_dispatch(const NormPlan& p, int dtype, F f) {
     using std::integral_constant;
-    auto by_threads = [&](auto t, auto vec, auto nv) {
-        return p.s.threads <= lnorm::THREADS ? f(t, vec, nv, integral_constant<int, lnorm::THREADS>())
-               : p.s.threads <= 512          ? f(t, vec, nv, integral_constant<int, 512>())
-                                             : f(t, vec, nv, integral_constant<int, 1024>());
+    auto by_threads = [&](auto t, auto vec, auto nv) -> int {
+        constexpr bool most = vec() * nv() == lnorm::MAX_EPT;
+        if (p.s.threads <= lnorm::THREADS) return f(t, vec, nv, integral_constant<int, lnorm::THREADS>());
+        if constexpr (BWD || most)
+            if (p.s.threads <= 512) return f(t, vec, nv, integral_constant<int, 512>());
+        if constexpr (most) return f(t, vec, nv, integral_constant<int, 1024>());
+        return TTT_ERR_UNSUPPORTED;
     };
     auto by_nv = [&](auto t, auto vec) -> int {
         constexpr int V = decltype(vec)::value;
@@ -1247,6 +1251,7 @@ int lin_orth(const void* q, const void* k, const void* v, const float* w0, void*
 
 }  // namespace
 
+// ====================================================================== C ABI ==========
 extern "C" {
 
 const char* ttt_status_string(int status) {
@@ -1732,7 +1737,7 @@ int ttt_layernorm(const void* x, const float* gamma, const float* beta, void* y,
     const int rpb = p.s.rows_per_block();
     DeviceInfo* dev = nullptr;
     if (int rc = current_device(&dev)) return rc;
-    return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv, auto maxt) {
+    return norm_dispatch<false>(p, dtype, [&](auto t, auto vec, auto nv, auto maxt) {
         using T = decltype(t);
         // rows of a thread in flight: up to 32 elements of it (4 rows at most), one while that leaves SMs
         // without two blocks
@@ -1770,7 +1775,7 @@ int ttt_layernorm_bwd(const void* dy, const void* x, const float* gamma, void* d
     const int sums = rpb > 1 ? rpb * 2 * C * 4 : 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     float* part = static_cast<float*>(workspace);
-    return norm_dispatch(p, dtype, [&](auto t, auto vec, auto nv, auto maxt) {
+    return norm_dispatch<true>(p, dtype, [&](auto t, auto vec, auto nv, auto maxt) {
         using T = decltype(t);
         using Ahead = lnorm::Ahead<T, vec(), nv(), maxt()>;
         const auto kern = lnorm::backward_kernel<T, vec(), nv(), maxt()>;
@@ -1835,10 +1840,8 @@ int ttt_rope(const void* q, const void* k, void* q_out, void* k_out, const float
     if (k && k == k_out && (s[1][0] != s[3][0] || s[1][1] != s[3][1] || s[1][2] != s[3][2])) return TTT_ERR_INVALID_ARG;
     p.pos = pos;
     p.pos_b = pos && pos_batched ? (long long)N * axes : 0;
-    p.B = B;
     p.H = H;
     p.N = N;
-    p.d = d;
     p.ax.n = axes;
     p.ax.pairs = at / 2;
     p.interleaved = interleaved != 0;

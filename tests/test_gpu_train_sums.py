@@ -78,3 +78,31 @@ def test_weight_sums_past_32_bit_offsets():
     assert torch.equal(dbeta.double(), want)
     want[1::2] *= -1
     assert torch.equal(dgamma.double(), want)
+
+
+WIDTHS = [*range(1, 140), *range(140, 600, 7), *range(600, 16384, 331), 255, 256, 257, 384, 385, 511, 512, 513, 1023, 1024, 1025, 2048,
+          2052, 4096, 4097, 4100, 8191, 8192, 8193, 8196, 8200, 12000, 16368, 16376, 16380, 16383, 16384]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [3, 1200])
+def test_every_width_has_its_kernels(rows, dtype):
+    # dbeta of whole numbers is exact; y and dx of such rows against the definition
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    for C in WIDTHS:
+        x = torch.randn(rows, C, generator=g, device=DEV).to(DT[dtype])
+        dy = torch.randint(-3, 4, (rows, C), generator=g, device=DEV).to(DT[dtype])
+        gamma = torch.ones(C, device=DEV)
+        y = ttt.layernorm(x, gamma, eps=1.0)
+        dx, _, dbeta = ttt.layernorm_bwd(dy, x, gamma, eps=1.0)
+        assert torch.equal(dbeta, dy.double().sum(0).float()), C
+        c = x.double() - x.double().mean(1, keepdim=True)
+        rstd = (c.square().mean(1, keepdim=True) + 1.0).rsqrt()
+        xh, d = c * rstd, dy.double()
+        want = rstd * (d - d.mean(1, keepdim=True) - xh * (d * xh).mean(1, keepdim=True))
+        # a half step of the output for every value, and 64 roundings of fp32 of what a row's values reach (|xh| and
+        # |dy| up to 8 here, rstd at most 1)
+        h = 2.0 ** -24 if dtype == "f32" else 2.0 ** -8
+        assert ((y.double() - xh).abs() <= h * xh.abs() + 64 * 2.0 ** -24 * 8).all(), C
+        assert ((dx.double() - want).abs() <= h * want.abs() + 64 * 2.0 ** -24 * 8 * 8).all(), C
+    assert ttt.device_error() == 0
