@@ -800,6 +800,10 @@ NormPlan norm_plan(int C, int dtype) {
     const int vecs = C / p.vec, most = lnorm::MAX_EPT / p.vec;
     p.nv = most;
     while (p.nv > 1 && p.nv * 16 > vecs) p.nv /= 2;  // short rows: a lane per vector first
+    // Single elements, a warp to a row of up to 384: twelve a thread leave room for more rows in registers than
+    // sixteen (12001 x 301 and x 383: fp32 forward 9.7 and 11.1 us against 13.4 and 14.9, backward 18.2 and 19.2 against
+    // 21.6 and 22.6; bf16 backward 15.9 and 16.5 against 30.3 and 33.2, where sixteen spill).  Ten up to 320 and
+    // fourteen up to 448 as well: within 6 % of this, but for 445 to 447 forward (12.8 against 16.1).
     if (p.nv == 16 && (vecs + 31) / 32 <= 12) p.nv = 12;
     const int need = (vecs + p.nv - 1) / p.nv;
     if (need <= 32) {
