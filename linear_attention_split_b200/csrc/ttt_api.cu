@@ -802,8 +802,8 @@ NormPlan norm_plan(int C, int dtype) {
     while (p.nv > 1 && p.nv * 16 > vecs) p.nv /= 2;  // short rows: a lane per vector first
     // Single elements, a warp to a row of up to 384: twelve a thread leave room for more rows in registers than
     // sixteen (12001 x 301 and x 383: fp32 forward 9.7 and 11.1 us against 13.4 and 14.9, backward 18.2 and 19.2 against
-    // 21.6 and 22.6; bf16 backward 15.9 and 16.5 against 30.3 and 33.2, where sixteen spill).  Ten up to 320 and
-    // fourteen up to 448 as well: within 6 % of this, but for 445 to 447 forward (12.8 against 16.1).
+    // 21.6 and 22.6; bf16 backward 15.9 and 16.5 against 30.3 and 33.2, where sixteen spill).  Ten up to 320 as well:
+    // 6 % less backward, 22 % more for bf16 forward; fourteen up to 448: 20 % less forward, 8 % more for fp32 backward.
     if (p.nv == 16 && (vecs + 31) / 32 <= 12) p.nv = 12;
     const int need = (vecs + p.nv - 1) / p.nv;
     if (need <= 32) {
@@ -962,11 +962,11 @@ int orth_check(int steps, float a, float b, float c, float eps) {
 // A product's tile width and split of K over a cluster, the fastest by count: K blocks at their cycles
 // (Config::BLOCK), a tile's start and end about 3000 and 35 a column (7 more accumulators: as much again),
 // the exchange of a split tile about 2000 and 20 a column (500 and 10 while half of the SMs are idle: 384 x
-// 384 times itself in two halves 97 us for all steps of 384 x 1536, unsplit 101), and 148 SMs holding 148, 72, 33 or 15 clusters of
-// 1, 2, 4 or 8.  Full precision takes no more than `most` MMAs into one accumulator where it can: 24 for fp32
-// matrices (error of 1500 x 4096, 2048 x 2048 and 2048 x 8192 5.4e-6, 7.5e-6 and 5.9e-6 of the norm; with 50 it was
-// 14e-6, 15e-6 and 22e-6, with 20 1.05e-5 for 4096 x 4096 and 15 % more time for 1024 x 4096), 50 for bf16 ones, whose
-// own rounding is a hundred times that.
+// 384 times itself in two halves 97 us for all steps of 384 x 1536, unsplit 101), and 148 SMs holding 148,
+// 72, 33 or 15 clusters of 1, 2, 4 or 8 (other numbers of SMs in proportion).  Full precision takes no more than
+// `most` MMAs into one accumulator where it can: 24 for fp32 matrices (error of 1500 x 4096, 2048 x 2048 and
+// 2048 x 8192 5.4e-6, 7.5e-6 and 5.9e-6 of the norm; with 50 it was 14e-6, 15e-6 and 22e-6, with 20 1.05e-5 for
+// 4096 x 4096 and 15 % more time for 1024 x 4096), 50 for bf16 ones, whose own rounding is a hundred times that.
 struct OrthPick {
     int bn = 0, S = 0;
     long long cycles = 0;
@@ -979,12 +979,12 @@ int orth_tiles(bool symmetric, int M, int cols, int bn) {
     return t;
 }
 template <typename C>
-void orth_consider(OrthPick& best, int tiles, long long U, int kblocks, int most) {
-    const int room[4] = {148, 72, 33, 15};
+void orth_consider(OrthPick& best, int tiles, long long U, int kblocks, int most, int sms) {
+    const int room[4] = {sms, std::max(1, sms * 72 / 148), std::max(1, sms * 33 / 148), std::max(1, sms * 15 / 148)};
     for (int i = 0, S = 1; i < (C::EXCHANGE ? 4 : 1); ++i, S *= 2) {
         if (S > 1 && kblocks < 2 * S) break;
         const long long per = (kblocks + S - 1) / S, waves = (tiles * U + room[i] - 1) / room[i];
-        const long long exchange = tiles * U * S <= 74 ? 500 + 10 * C::BN : 2000 + 20 * C::BN;
+        const long long exchange = tiles * U * S <= sms / 2 ? 500 + 10 * C::BN : 2000 + 20 * C::BN;
         long long cycles = waves * (per * C::BLOCK + 3000 + 35 * C::BN + (S > 1 ? exchange : 0));
         if (C::FL && per * 4 > most * C::ACC) cycles *= 2;
         if (!best.bn || cycles < best.cycles) {
@@ -1033,12 +1033,12 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
     auto consider = [&](auto bn) {
         constexpr int BN = bn();
         if constexpr (BN <= 128) {
-            orth_consider<orth::Full<BN>>(pick[0][0], orth_tiles(true, p.M, p.M, BN), U, kx, most);
-            orth_consider<orth::Full<BN>>(pick[0][1], orth_tiles(true, p.M, p.M, BN), U, km, most);
-            orth_consider<orth::Full<BN>>(pick[0][2], orth_tiles(false, p.M, p.N, BN), U, km, most);
-            orth_consider<orth::High<BN>>(pick[1][0], orth_tiles(true, p.M, p.M, BN), U, kx, most);
+            orth_consider<orth::Full<BN>>(pick[0][0], orth_tiles(true, p.M, p.M, BN), U, kx, most, dev->sms);
+            orth_consider<orth::Full<BN>>(pick[0][1], orth_tiles(true, p.M, p.M, BN), U, km, most, dev->sms);
+            orth_consider<orth::Full<BN>>(pick[0][2], orth_tiles(false, p.M, p.N, BN), U, km, most, dev->sms);
+            orth_consider<orth::High<BN>>(pick[1][0], orth_tiles(true, p.M, p.M, BN), U, kx, most, dev->sms);
         }
-        orth_consider<orth::High<BN>>(pick[1][2], orth_tiles(false, p.M, p.N, BN), U, km, most);
+        orth_consider<orth::High<BN>>(pick[1][2], orth_tiles(false, p.M, p.N, BN), U, km, most, dev->sms);
     };
     consider(std::integral_constant<int, 64>());
     consider(std::integral_constant<int, 128>());
