@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 import re
 
@@ -538,13 +539,18 @@ def _rope(q, k, q_out, k_out, pos, base, interleaved, inverse, stream, args):
           inverse, strides, dt)
 
 
+def _whole(sizes):
+    """Plain integers, which is what the checks' answers are kept by (an integer tensor would go by its identity)."""
+    return None if sizes is None else tuple(map(operator.index, sizes))
+
+
 def ttt_rope(q, k, q_out, k_out, dims, grid=None, pos=None, base=10000.0, interleaved=False, inverse=False, stream=None):
     """Rotary positions: q, k and their outputs [B, H, N, d], any strides with adjacent features (k, k_out may be
     None; an output may be its own input).  dims: the even widths of the axes' sections.  Either grid, the sizes of
     the token grid, or pos, fp32 [N, axes] or [B, N, axes].  inverse: turn back, which is the backward pass."""
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    args = _rope_args(_sig(q), _sig(k), _sig(q_out), _sig(k_out), _sig(pos), tuple(dims), None if grid is None else tuple(grid))
+    args = _rope_args(_sig(q), _sig(k), _sig(q_out), _sig(k_out), _sig(pos), _whole(dims), _whole(grid))
     _rope(q, k, q_out, k_out, pos, base, interleaved, inverse, stream, args)
     return q_out, k_out
 
@@ -705,7 +711,7 @@ def layernorm_bwd(dy, x, gamma, eps=1e-6, with_dbeta=True):
 
 def rope(q, k=None, dims=None, grid=None, pos=None, base=10000.0, interleaved=False, inverse=False):
     """q and k turned to their positions, each contiguous [B, H, N, d]; without k, q alone."""
-    args = _rope_args(_sig(q), _sig(k), None, None, _sig(pos), tuple(dims), None if grid is None else tuple(grid))
+    args = _rope_args(_sig(q), _sig(k), None, None, _sig(pos), _whole(dims), _whole(grid))
     q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
     _rope(q, k, q_out, k_out, pos, base, interleaved, inverse, None, args)

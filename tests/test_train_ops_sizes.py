@@ -76,3 +76,23 @@ def test_layernorm_bwd_workspace_of_the_most_rows(C, dtype):
     assert 0 < few <= 2 * 256 * 2 * C * 4
     for rows in (2 ** 31 - 600, 2 ** 31 - 512, 2 ** 31 - 256, 2 ** 31 - 2, 2 ** 31 - 1):
         assert ttt.ttt_layernorm_bwd_workspace_bytes(rows, C, dtype) == few
+
+
+def test_rope_axes_are_taken_by_value(monkeypatch):
+    # widths and grid sizes held in integer tensors that change between calls
+    seen = []
+    monkeypatch.setattr(ttt, "_sig_device", lambda *sigs: 0)
+    monkeypatch.setattr(ttt, "_call", lambda fn, dev, stream, *args: seen.append((list(args[6]), list(args[7]))))
+    monkeypatch.setattr(ttt, "lib", lambda: type("L", (), {"ttt_rope": None}))
+    q = meta(1, 2, 12, 8)
+    dims, grid = (torch.tensor(4), torch.tensor(2)), (torch.tensor(3), torch.tensor(4))
+    ttt.rope(q, q, dims, grid=grid)
+    dims[1].fill_(4)
+    grid[0].fill_(6)
+    grid[1].fill_(2)
+    ttt.rope(q, q, dims, grid=grid)
+    assert seen == [([3, 4], [4, 2]), ([6, 2], [4, 4])]
+    for bad in ((4.0, 2.0), ("4", "2")):  # also after the same whole numbers were taken
+        with pytest.raises(TypeError):
+            ttt.rope(q, q, bad, grid=(3, 4))
+    ttt._rope_args.cache_clear()
