@@ -13,7 +13,7 @@
 // fraction (error about 1e-7).  A block does this once per (token, pair) of its token tile and
 // keeps the table in shared memory for its heads and both tensors.
 //
-// The bound is HBM (one read and one write of Q and K).  A thread takes VEC adjacent pairs: two
+// The floor is HBM (one read and one write of Q and K); what bounds it is the latency of the loads.  A thread takes VEC adjacent pairs: two
 // loads of VEC features (16 bytes each where dims, strides and pointers are multiples of 16 bytes;
 // the largest power of two that divides them all otherwise), two table reads, two stores.  A unit
 // (its place in the head) is fixed for a thread; it walks rows, several loads in flight, and finds a row's head
