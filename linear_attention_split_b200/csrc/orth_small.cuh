@@ -3,10 +3,15 @@
 //
 // A matrix of at most 64 rows stays in shared memory through all steps, so nothing but the input and
 // the result touches HBM.  Each operand lies there as 128 rows, 64 of hi and 64 of lo (fp16, as in
-// orth.cuh), and one tcgen05 product of the stacked rows, [hi; lo] [hi | lo], gives hi hi, hi lo and
-// lo hi at once as quarters of a 128 x 128 accumulator: four MMAs of K = 16 for a 64 x 64 x 64 product,
-// 268 cycles.  lo hi sits in the lanes that the other warps can read, so each side of the block sends the
-// other side's columns through shared memory; a thread finishes 16 columns of a row.
+// orth.cuh), and one tcgen05 product of the stacked rows, [hi; lo] [hi | lo], gives hi hi, hi lo, lo hi and
+// lo lo at once as quarters of a 128 x 128 accumulator: four MMAs of K = 16 for a 64 x 64 x 64 product,
+// 268 cycles.  lo hi and lo lo sit in the lanes that the other warps can read, so each side of the block sends
+// the other side's columns through shared memory; a thread finishes 16 columns of a row.
+//
+// X <- a X + P X with P = b A + c A^2: a X is added in fp32, so that the accumulator cuts and P's storage rounds only
+// what the step adds, little in the first steps, whose errors are enlarged most.  With a in P's diagonal, and lo lo
+// left out, fp32 results were 1.3 to 2.5 times as far off as the same steps in plain fp32: 64 x 64 1.9e-6 of the norm
+// against 1.2e-6, 64 x 256 3.7e-6 against 1.5e-6; now 1.0e-6 and 2.4e-6 (two accumulators for X X^T: 2.2e-6).
 //
 // The bound is latency: a step is three such products, each waiting for the one before (accumulator
 // out of tensor memory, exchange, rounding to hi + lo, operand written, MMAs; about 1400 cycles).  Several
@@ -43,6 +48,19 @@ __device__ __forceinline__ void put_op8(uint8_t* op, int row, int col, const flo
     uint8_t* at = op + swz<3>((uint32_t)row * 128 + (uint32_t)col * 2);
     *reinterpret_cast<uint4*>(at) = make_uint4(h0.x, h0.y, h1.x, h1.y);
     *reinterpret_cast<uint4*>(at + SM_M * 128) = make_uint4(l0.x, l0.y, l1.x, l1.y);
+}
+
+// what an operand holds there, hi + lo
+__device__ __forceinline__ void get_op8(const uint8_t* op, int row, int col, float* v) {
+    const uint8_t* at = op + swz<3>((uint32_t)row * 128 + (uint32_t)col * 2);
+    const uint4 h = *reinterpret_cast<const uint4*>(at), l = *reinterpret_cast<const uint4*>(at + SM_M * 128);
+    const uint32_t hi[4] = {h.x, h.y, h.z, h.w}, lo[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&hi[e])), b = __half22float2(*reinterpret_cast<const __half2*>(&lo[e]));
+        v[2 * e] = a.x + b.x;
+        v[2 * e + 1] = a.y + b.y;
+    }
 }
 
 // What a block works with
@@ -82,32 +100,27 @@ struct Small {
         tc::fence_after();
     }
     // The row and the first of the 16 columns that a thread finishes: warps 0, 1, 4, 5 read the lanes of hi hi
-    // and hi lo and finish columns 0 .. 31, the others read those of lo hi and finish columns 32 .. 63.
+    // and hi lo and finish columns 0 .. 31, the others read those of lo hi and lo lo and finish columns 32 .. 63.
     static __device__ __forceinline__ int row() { return (threadIdx.x >> 5 & 1) * 32 + (threadIdx.x & 31); }
     static __device__ __forceinline__ int col() { return (threadIdx.x >> 6 & 1) * 32 + (threadIdx.x >> 7) * 16; }
-    // v: the thread's values of hi hi + hi lo + lo hi
+    // v: the thread's values of hi hi + hi lo + lo hi + lo lo
     __device__ __forceinline__ void take(float (&v)[16]) {
         mbar_wait<false>(&bars->done, products++ & 1, TTT_DEVERR_TIMEOUT_TMA);
         tc::fence_after();
         const int warp = threadIdx.x >> 5, side = warp >> 1 & 1, c0 = (warp >> 2) * 16;
         const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
-        float s[16];  // for the other side
-        if (side == 0) {
-            float h[16], l[16];
-            tc::ld16(at, v);
-            tc::ld16(at + 32, s);
-            tc::ld16(at + 64, h);
-            tc::ld16(at + 96, l);
-            tc::wait_ld();
+        // this side's columns and the other side's: side 0 keeps the first half and sends the second
+        const uint32_t mine = at + 32 * side, theirs = at + 32 - 32 * side;
+        float s[16], h[16], l[16];
+        tc::ld16(mine, v);
+        tc::ld16(theirs, s);
+        tc::ld16(mine + 64, h);
+        tc::ld16(theirs + 64, l);
+        tc::wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                v[c] += h[c];
-                s[c] += l[c];
-            }
-        } else {
-            tc::ld16(at, s);
-            tc::ld16(at + 32, v);
-            tc::wait_ld();
+        for (int c = 0; c < 16; ++c) {
+            v[c] += h[c];
+            s[c] += l[c];
         }
         float* out = ex + (side * 32 + c0) * SM_M + row();  // [column][row]
         const float* in = ex + ((1 - side) * 32 + c0) * SM_M + row();
@@ -125,7 +138,7 @@ struct Small {
         const int row = this->row(), col = this->col();
         const uint64_t xk = tc::smem_desc(smem_u32(X), 16, 1024, 2), xn = tc::smem_desc(smem_u32(X), SM_M * 128, 1024, 2);
         const uint64_t ak = tc::smem_desc(smem_u32(A), 16, 1024, 2);
-        const float pa = SP * ca, pb = SP / SX * cb, pc = SP / (SX * SX) * cc;  // P = SP (a I + b A + c A^2)
+        const float pa = SP * ca, pb = SP / SX * cb, pc = SP / (SX * SX) * cc;  // P = SP (b A + c A^2)
         for (int k = 0; k < count; ++k) {
             float v[16], a[16];
             written();
@@ -151,7 +164,7 @@ struct Small {
             }
             take(v);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = fmaf(pc, v[c], pb * a[c]) + (row == col + c ? pa : 0.f);
+            for (int c = 0; c < 16; ++c) v[c] = fmaf(pc, v[c], pb * a[c]);
 #pragma unroll
             for (int c = 0; c < 16; c += 8) put_op8(A, row, col + c, v + c);
             const bool done = k + 1 == count;
@@ -164,6 +177,10 @@ struct Small {
                     tc::commit(&bars->done);
                 }
                 take(v);
+                get_op8(X + s * SM_OP, row, col, a);
+                get_op8(X + s * SM_OP, row, col + 8, a + 8);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v[c] = fmaf(pa, a[c], v[c]);
                 if (done) {
                     last(row, 64 * s + col, v);
                 } else {

@@ -112,3 +112,21 @@ def test_f32_of_random_matrices_is_as_good_as_promised(U, m, n):
     x = torch.randn(U, m, n, generator=g, device=DEV)
     x += torch.randn(U, m, 1, generator=g, device=DEV) @ torch.randn(U, 1, n, generator=g, device=DEV)
     assert error(x, ttt.orthogonalize(x)) <= (5e-6 if U == 1 and min(m, n) <= 1024 else 1e-5)
+
+
+# Small fp32 matrices, the error of 24 of them together.  A step stores X, A and P to 22 bits, 2^-22 / sqrt(3) = 1.4e-7 of
+# their norms each, sqrt(3) x 1.4e-7 = 2.4e-7 for a step, and gains of about 2 over the steps that follow for these
+# spectra: sqrt(5) x 2 x 2.4e-7 = 1.1e-6; cut additions of X X^T add 2^-24 for each of up to 16, in its share of the step:
+# 1e-6 for 256 columns.  With a in P's diagonal, where the accumulator cuts all of a X, 33 x 64 is 2.5e-6 off, 45 x 81 2.6e-6,
+# 64 x 200 3.4e-6 and 64 x 256 3.7e-6.
+@pytest.mark.parametrize("rank", [0, 3])
+@pytest.mark.parametrize("m,n,tol", [(64, 64, 2e-6), (33, 64, 2e-6), (17, 33, 2e-6), (45, 81, 2e-6), (81, 45, 2e-6), (64, 200, 3e-6), (64, 256, 3e-6),
+                                     (256, 64, 3e-6), (8, 8, 2e-6), (5, 7, 2e-6), (12, 100, 2e-6), (1, 9, 2e-6)])
+def test_f32_small_matrices(m, n, tol, rank):
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(24, m, n, generator=g, device=DEV)
+    if rank:
+        x += torch.randn(24, m, rank, generator=g, device=DEV) @ torch.randn(24, rank, n, generator=g, device=DEV)
+    want, got = steps64(x), ttt.orthogonalize(x).double()
+    got = got.mT if m > n else got
+    assert (got - want).norm() <= tol * want.norm()
