@@ -276,11 +276,10 @@ int ttt_linear_fullbatch_orth(const void* q, const void* k, const void* v, const
  *   x, out : [U, m, n] dtype (out may be x)
  * A zero matrix stays zero; one with a NaN or an infinity becomes NaN throughout.  With the usual
  * coefficients bf16 results are within 2^-8 of their norm whatever the spectrum (measured 1.5e-3 to
- * 2.3e-3, nearly all of it their own rounding).  fp32 results are good to 5e-6 of it, or 1e-5 for several
- * matrices or a shorter side above 1024, where no direction is much stronger than the rest (measured 1e-6 to
- * 3e-6, and 2e-6 to 7.5e-6).  Five steps enlarge a rounding along a small
- * singular value by up to a^5 = 485: with one direction 100 times the rest 7e-6 to 2e-5 were measured,
- * with 1000 times 4e-5 to 1.2e-4 (the same steps in plain fp32: 9e-6 to 4e-5 and 5e-5 to 2.1e-4); 22-bit
+ * 2.3e-3, nearly all of it their own rounding).  fp32 results are good to 5e-6 of it where no direction
+ * is much stronger than the rest (measured 1e-6 to 3.6e-6).  Five steps enlarge a rounding along a small
+ * singular value by up to a^5 = 485: with one direction 100 times the rest 7e-6 to 1.2e-5 were measured,
+ * with 1000 times 4e-5 to 7e-5 (the same steps in plain fp32: 9e-6 to 4e-5 and 5e-5 to 2.1e-4); 22-bit
  * roundings of five steps bound it at 5.8e-4 over the result's norm.  Errors:
  * steps outside 1..64, eps <= 0 or a non-finite number is TTT_ERR_INVALID_ARG; coefficients under
  * which a value in [0, 1] leaves [-2, 2] on the way (the iteration would run away), U > 65535,

@@ -28,7 +28,10 @@
 // MN-major operand.  The tensor cores cut what falls below the accumulator's last bit at every
 // addition, about 1e-7 of the result for each: a full product therefore spreads its K blocks over
 // three or seven accumulators and keeps the cross terms in another, added in fp32 in the epilogue
-// (1024 x 4096, one accumulator: 2.4e-5 of the norm).
+// (1024 x 4096, one accumulator: 1.3e-5 of the norm, now 2.7e-6), and A Q and P X take the K blocks of a tile's own rows
+// last: A's and P's diagonals make their sums large, and all that is added to a large sum is cut.  (In ascending order
+// 4 x 1024 x 1024 was 8.0e-6 off, 2048 x 2048 1.5e-5 and 2048 x 8192 2.2e-5; now 3.0e-6, 3.1e-6 and 3.6e-6, the same steps in
+// plain fp32 2.6e-6, 3.3e-6 and 4.5e-6.)
 #pragma once
 #include "common.cuh"
 #include <cuda_fp16.h>
@@ -362,6 +365,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_con
     }
     const int i0 = bi * TM, j0 = bj * C::BN;  // the tile's place
     const int per = (p.kblocks + S - 1) / S, k0 = min(r * per, p.kblocks), nk = min(per, p.kblocks - k0);
+    // A Q and P X take the CTA's K blocks in a circle that ends with those of the tile's own rows, if they are among them
+    int turn = 0;
+    if (KIND >= POLY) {
+        const int last = min(2 * bi + 1, p.kblocks - 1) - k0;
+        if (last >= 0 && last < nk) turn = last + 1 < nk ? last + 1 : 0;
+    }
     // accumulators for hi hi: `used` of them, each for a run of `len` of the 4 nk MMAs (hi hi alone: one for
     // each issuer)
     const int len = (4 * nk + C::ACC - 1) / C::ACC;
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_con
         bool ready = false;
         constexpr int FROM = C::CROSS ? 0 : j, STEP = C::CROSS ? 1 : 2;
         for (int i = FROM; i < nk; i += STEP) {
-            const int slot = i % C::STAGES, t = (k0 + i) * KB / TM;
+            const int slot = i % C::STAGES, t = (k0 + (i + turn < nk ? i + turn : i + turn - nk)) * KB / TM;
             if (!ready) mbar_wait(&bars->full[slot], (i / C::STAGES) & 1, TTT_DEVERR_TIMEOUT_TMA);
             const int n = i + STEP;  // the next block's phase is asked for ahead of this block's MMAs
             ready = n < nk && mbar_test_wait(&bars->full[n % C::STAGES], (n / C::STAGES) & 1);
@@ -433,7 +442,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) product_kernel(const __grid_con
                 if (use > 0) mbar_wait(&bars->empty[slot], (use - 1) & 1, TTT_DEVERR_TIMEOUT_TMA);
                 uint8_t* dst = ring + slot * C::STAGE;
                 uint64_t* bar = &bars->full[slot];
-                const int k = (k0 + i) * KB;
+                const int k = (k0 + (i + turn < nk ? i + turn : i + turn - nk)) * KB;
                 mbar_expect_tx(bar, C::STAGE);
                 for (int part = 0; part < 1 + C::FL; ++part, dst += OPB) {
                     if (KIND == GRAM)

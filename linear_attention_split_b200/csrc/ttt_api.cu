@@ -964,9 +964,7 @@ int orth_check(int steps, float a, float b, float c, float eps) {
 // the exchange of a split tile about 2000 and 20 a column (500 and 10 while half of the SMs are idle: 384 x
 // 384 times itself in two halves 97 us for all steps of 384 x 1536, unsplit 101), and 148 SMs holding 148,
 // 72, 33 or 15 clusters of 1, 2, 4 or 8 (other numbers of SMs in proportion).  Full precision takes no more than
-// `most` MMAs into one accumulator where it can: 24 for fp32 matrices (error of 1500 x 4096, 2048 x 2048 and
-// 2048 x 8192 5.4e-6, 7.5e-6 and 5.9e-6 of the norm; with 50 it was 14e-6, 15e-6 and 22e-6, with 20 1.05e-5 for
-// 4096 x 4096 and 15 % more time for 1024 x 4096), 50 for bf16 ones, whose own rounding is a hundred times that.
+// 50 MMAs into one accumulator where it can.
 struct OrthPick {
     int bn = 0, S = 0;
     long long cycles = 0;
@@ -979,14 +977,14 @@ int orth_tiles(bool symmetric, int M, int cols, int bn) {
     return t;
 }
 template <typename C>
-void orth_consider(OrthPick& best, int tiles, long long U, int kblocks, int most, int sms) {
+void orth_consider(OrthPick& best, int tiles, long long U, int kblocks, int sms) {
     const int room[4] = {sms, std::max(1, sms * 72 / 148), std::max(1, sms * 33 / 148), std::max(1, sms * 15 / 148)};
     for (int i = 0, S = 1; i < (C::EXCHANGE ? 4 : 1); ++i, S *= 2) {
         if (S > 1 && kblocks < 2 * S) break;
         const long long per = (kblocks + S - 1) / S, waves = (tiles * U + room[i] - 1) / room[i];
         const long long exchange = tiles * U * S <= sms / 2 ? 500 + 10 * C::BN : 2000 + 20 * C::BN;
         long long cycles = waves * (per * C::BLOCK + 3000 + 35 * C::BN + (S > 1 ? exchange : 0));
-        if (C::FL && per * 4 > most * C::ACC) cycles *= 2;
+        if (C::FL && per * 4 > 50 * C::ACC) cycles *= 2;
         if (!best.bn || cycles < best.cycles) {
             best.bn = C::BN;
             best.S = S;
@@ -1029,16 +1027,15 @@ int orth_run(const T* x, T* out, long long U, int m, int n, int steps, float a, 
     // the three products' tiles, in full [0] and of the hi parts alone [1]
     const int kx = (p.N + orth::KB - 1) / orth::KB, km = (p.M + orth::KB - 1) / orth::KB;
     OrthPick pick[2][3];
-    constexpr int most = kHalf ? 50 : 24;
     auto consider = [&](auto bn) {
         constexpr int BN = bn();
         if constexpr (BN <= 128) {
-            orth_consider<orth::Full<BN>>(pick[0][0], orth_tiles(true, p.M, p.M, BN), U, kx, most, dev->sms);
-            orth_consider<orth::Full<BN>>(pick[0][1], orth_tiles(true, p.M, p.M, BN), U, km, most, dev->sms);
-            orth_consider<orth::Full<BN>>(pick[0][2], orth_tiles(false, p.M, p.N, BN), U, km, most, dev->sms);
-            orth_consider<orth::High<BN>>(pick[1][0], orth_tiles(true, p.M, p.M, BN), U, kx, most, dev->sms);
+            orth_consider<orth::Full<BN>>(pick[0][0], orth_tiles(true, p.M, p.M, BN), U, kx, dev->sms);
+            orth_consider<orth::Full<BN>>(pick[0][1], orth_tiles(true, p.M, p.M, BN), U, km, dev->sms);
+            orth_consider<orth::Full<BN>>(pick[0][2], orth_tiles(false, p.M, p.N, BN), U, km, dev->sms);
+            orth_consider<orth::High<BN>>(pick[1][0], orth_tiles(true, p.M, p.M, BN), U, kx, dev->sms);
         }
-        orth_consider<orth::High<BN>>(pick[1][2], orth_tiles(false, p.M, p.N, BN), U, km, most, dev->sms);
+        orth_consider<orth::High<BN>>(pick[1][2], orth_tiles(false, p.M, p.N, BN), U, km, dev->sms);
     };
     consider(std::integral_constant<int, 64>());
     consider(std::integral_constant<int, 128>());

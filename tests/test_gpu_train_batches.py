@@ -35,7 +35,7 @@ def test_small_matrices_by_themselves_and_among_many(m, n, dtype):
         assert torch.equal(ttt.orthogonalize(x[u:u + 1].clone())[0], got[u])
 
 
-@pytest.mark.parametrize("dtype,tol", [("f32", 1e-5), ("bf16", 2.0 ** -8)])
+@pytest.mark.parametrize("dtype,tol", [("f32", 5e-6), ("bf16", 2.0 ** -8)])
 @pytest.mark.parametrize("m,n", [(130, 257), (384, 512), (257, 64)])
 def test_large_matrices_by_themselves_and_among_many(m, n, dtype, tol):
     x = randn(40, m, n, seed=m + n).to(DT[dtype])
