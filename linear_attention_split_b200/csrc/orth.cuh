@@ -14,7 +14,7 @@
 // step a direction 30, 100 or 1000 times the rest left 0.8, 2 or 9 % of the result's norm wrong.  In the last
 // step (the last ones whose slopes multiply to at most 4: orth_high_from) X and P are held as hi alone and only
 // A Q is taken in full, which costs less than rounding the result to bf16, whatever the spectrum (1.5e-3 to
-// 2.3e-3 in all, measured; 1024 x 4096: 236 us, with hi alone at every step 157, in full throughout 263).
+// 2.3e-3 in all, measured; 1024 x 4096: 238 us, with hi alone at every step 157, in full throughout 263).
 // Values are bounded (|s| <= 2 throughout, checked on the host), so fixed powers of two keep them inside fp16:
 // X and A are stored times 2^12, P times 2^10, Q times 2^9.
 //
